@@ -338,6 +338,162 @@ ssd_status_t ssd_fwd_noalloc(const ssd_shape_t *shape, ssd_dtype_t io,
                              const float *init_states,
                              void *y, float *final_states, void *stream);
 
+/* ---- Layer operators around the scan -----------------------------------
+ *
+ * What a recurrent layer runs next to ssd_fwd, for training (forward and
+ * backward) and for serving (single-token forms): a gated linear recurrence
+ * over channels, the short causal depthwise convolution in front of a scan,
+ * and the root-mean-square norm before and after it.  Ownership, threading,
+ * errors and NaN/Inf as at the top of this file; every call may be captured
+ * in a HIP graph; every result is the same bit for bit on every call with
+ * the same inputs (no atomics; each sum in a fixed order).
+ *
+ * Layouts: activations [batch][seqlen][channels] (or [rows][columns]) with
+ * the channels of a token contiguous and a token stride: token t of row b
+ * starts at element (b seqlen + t) * stride.  A stride of 0 means dense
+ * (stride = channels).  This reads column slices of a projection's output in
+ * place.  Outputs and states are dense.  Activations need only the alignment
+ * of their type (16-byte aligned ones with a stride that keeps every token
+ * aligned are faster).  Outputs must not overlap inputs, except that
+ * residual_out may be the residual itself and a step's state is updated in
+ * place.  Channels, columns and strides are at most 2^20, tokens (batch
+ * seqlen, rows) at most 2^30 - 1. */
+
+/* Gated linear recurrence.  Per channel c, with the same decay map and
+ * document resets as ssd_fwd:
+ *   s_t = softplus(g_t + bias_c)       a_t = exp(A_c s_t)
+ *   h_t = r_t a_t h_{t-1} + k_t x_t    k_t = sqrt(1 - a_t^2) if normalize, else 1
+ *   y_t = h_t, or h_t silu(z_t) when z is given
+ * r_t = 0 where seq_idx changes between tokens t-1 and t, else 1; the state
+ * before token 0 is init_states (0 when NULL); final_states is the state
+ * after the row's last token.  States in fp32, all arithmetic in fp32. */
+typedef struct {
+    int64_t batch, seqlen, channels;
+    int64_t x_stride, g_stride, z_stride, dy_stride; /* tokens; 0 = dense */
+    int64_t normalize;    /* 0 or 1                                       */
+    int64_t reserved[4];  /* must be zero                                 */
+} ssd_glr_shape_t;
+
+/* Device workspace of ssd_glr_fwd (0: none), 16-byte aligned, queried with
+ * the device that will run the call current: 8 bytes per channel, row and
+ * sequence split, when rows and channels alone do not fill the device. */
+size_t ssd_glr_fwd_workspace_bytes(const ssd_glr_shape_t *shape, ssd_dtype_t io);
+
+/* x, g, z (nullable), y: io dtype; A (<= 0), bias (nullable): [channels]
+ * fp32; seq_idx [batch][seqlen] int32, nullable; init_states, final_states
+ * [batch][channels] fp32, nullable. */
+ssd_status_t ssd_glr_fwd(const ssd_glr_shape_t *shape, ssd_dtype_t io,
+                         const void *x, const void *g, const float *A, const float *bias,
+                         const void *z, const int32_t *seq_idx, const float *init_states,
+                         void *y, float *final_states,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of ssd_glr_fwd: the gradients of J = <dy, y> + <dfinal,
+ * final_states>, the states recomputed from the inputs.  dy, dx, dg, dz in
+ * the io dtype (dz exactly when z is given); dfinal (nullable), dinit
+ * (nullable; only with init_states) [batch][channels], dA, dbias (exactly
+ * when bias is given) [channels]: fp32.  Where k_t = 0 its derivative is
+ * taken as 0.  Workspace: ssd_glr_bwd_workspace_bytes, 16-byte aligned:
+ * 20 bytes per channel, row and 128-token block. */
+size_t ssd_glr_bwd_workspace_bytes(const ssd_glr_shape_t *shape, ssd_dtype_t io);
+ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io,
+                         const void *x, const void *g, const float *A, const float *bias,
+                         const void *z, const int32_t *seq_idx, const float *init_states,
+                         const void *dy, const float *dfinal,
+                         void *dx, void *dg, void *dz, float *dA, float *dbias, float *dinit,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of the recurrence (shape->seqlen must be 1): state [batch]
+ * [channels] fp32 is updated in place. */
+ssd_status_t ssd_glr_step(const ssd_glr_shape_t *shape, ssd_dtype_t io,
+                          const void *x, const void *g, const float *A, const float *bias,
+                          const void *z, float *state, void *y, void *stream);
+
+/* Causal depthwise convolution of width W = 2, 3 or 4:
+ *   p_t = bias_c + sum_{j < W} weight[c][W-1-j] x_{t-j},  y_t = silu(p_t) if silu, else p_t
+ * x before the row is the window init_states (its last entry is token -1; 0
+ * when NULL), and 0 across a document start (as r_t = 0 above); init_states
+ * feeds only the first document.  final_states is the window that the next
+ * token of the row's last document sees (0 before that document's start).
+ * Sums in fp32. */
+typedef struct {
+    int64_t batch, seqlen, channels, width;
+    int64_t x_stride, dy_stride;  /* tokens; 0 = dense */
+    int64_t silu;                 /* 0 or 1            */
+    int64_t reserved[4];          /* must be zero      */
+} ssd_conv_shape_t;
+
+/* x, y, init_states, final_states (both nullable, [batch][W-1][channels]):
+ * io dtype; weight [channels][W], bias [channels] (nullable): fp32.
+ * No workspace. */
+ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, ssd_dtype_t io,
+                          const void *x, const float *weight, const float *bias,
+                          const int32_t *seq_idx, const void *init_states,
+                          void *y, void *final_states, void *stream);
+
+/* Backward of ssd_conv_fwd.  dy, dx: io dtype; dfinal (nullable) and dinit
+ * (nullable; only with init_states) [batch][W-1][channels], dweight
+ * [channels][W], dbias (exactly when bias is given): fp32.  Workspace:
+ * ssd_conv_bwd_workspace_bytes, 16-byte aligned. */
+size_t ssd_conv_bwd_workspace_bytes(const ssd_conv_shape_t *shape, ssd_dtype_t io);
+ssd_status_t ssd_conv_bwd(const ssd_conv_shape_t *shape, ssd_dtype_t io,
+                          const void *x, const float *weight, const float *bias,
+                          const int32_t *seq_idx, const void *init_states,
+                          const void *dy, const float *dfinal,
+                          void *dx, float *dweight, float *dbias, float *dinit,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token (shape->seqlen must be 1): state [batch][W-1][channels] io dtype
+ * holds the last W-1 inputs and is shifted in place. */
+ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, ssd_dtype_t io,
+                           const void *x, const float *weight, const float *bias,
+                           void *state, void *y, void *stream);
+
+/* Root-mean-square norm of each row, in ngroups equal column groups:
+ *   v = x, or x silu(z) when z is given, or, when residual is given, the sum
+ *       x + residual rounded to the io dtype (written to residual_out)
+ *   y = v rsqrt(mean(v^2 over the group) + eps) weight
+ * residual and z exclude each other.  Statistics in fp32. */
+typedef struct {
+    int64_t rows, columns, ngroups;
+    int64_t x_stride, z_stride, residual_stride, dy_stride, dresidual_stride; /* rows; 0 = dense */
+    float eps;            /* > 0, finite                                        */
+    int32_t quant_block;  /* ssd_norm_quant_fwd: columns per scale, 128, or 0:
+                             one scale per norm group; 0 otherwise              */
+    int64_t reserved[4];  /* must be zero                                       */
+} ssd_norm_shape_t;
+
+/* x, z, residual, residual_out, y: io dtype; weight [columns] fp32, nullable
+ * (1).  residual_out is given exactly when residual is.  No workspace. */
+ssd_status_t ssd_norm_fwd(const ssd_norm_shape_t *shape, ssd_dtype_t io,
+                          const void *x, const float *weight, const void *residual,
+                          const void *z, void *y, void *residual_out, void *stream);
+
+/* The same with an 8-bit output.  For each block of quant_block columns
+ * (counted from its norm group's first column; the last one may be shorter):
+ *   m = max(max |y|, 1e-12),  scale = m / 448,  q = e4m3(y * (448 / m))
+ * from the unrounded fp32 y, rounded to nearest even; q [rows][columns] in
+ * the OCP e4m3 format without infinities, scales [rows][ngroups *
+ * ceil(columns / ngroups / quant_block)] fp32.  A NaN in a block makes its
+ * scale and its q NaN. */
+ssd_status_t ssd_norm_quant_fwd(const ssd_norm_shape_t *shape, ssd_dtype_t io,
+                                const void *x, const float *weight, const void *residual,
+                                const void *z, void *q, float *scales, void *residual_out,
+                                void *stream);
+
+/* Backward.  x is the normalised input (x, or residual_out of the forward
+ * call, which the norm saw), z as given forward; dresidual (nullable, not
+ * with z): the gradient of residual_out from its other uses, added to dx.
+ * dx, dz (exactly with z): io dtype, dense.  dx is the gradient of x and of
+ * the residual alike.  dweight [columns] fp32, exactly when weight is given.
+ * Workspace: ssd_norm_bwd_workspace_bytes (0 without weight), 16-byte
+ * aligned, queried with the device that will run the call current. */
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_shape_t *shape, ssd_dtype_t io);
+ssd_status_t ssd_norm_bwd(const ssd_norm_shape_t *shape, ssd_dtype_t io,
+                          const void *x, const float *weight, const void *z, const void *dy,
+                          const void *dresidual, void *dx, void *dz, float *dweight,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Debug exports (tests only) ---------------------------------------
  *
  * Segsum factor records.  The hierarchy-aware segsum (page "GPU Hierarchy

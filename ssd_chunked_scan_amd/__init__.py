@@ -21,6 +21,8 @@ from typing import Optional, Tuple
 __all__ = [
     "ssd_fwd", "prepare_fwd", "ssd_bwd", "ssd_fwd_workspace_bytes", "ssd_plan_split_len", "ssd_debug_chunk_mask",
     "ssd_decode_step",
+    "ssd_glr_fwd", "ssd_glr_bwd", "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step",
+    "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd",
     "SsdError", "library_path", "load_library", "STATUS", "EXPORTS",
 ]
 
@@ -37,6 +39,10 @@ EXPORTS = ["ssd_fwd_workspace_bytes", "ssd_fwd", "ssd_fwd_ex_workspace_bytes", "
            "ssd_decode_step", "ssd_decode_step_fused", "ssd_bwd_workspace_bytes", "ssd_bwd",
            "ssd_segsum_record_words", "ssd_debug_segsum_factors", "ssd_debug_fwd_segsum_factors",
            "ssd_debug_exp2_probe", "ssd_fwd_noalloc",
+           "ssd_glr_fwd_workspace_bytes", "ssd_glr_fwd", "ssd_glr_bwd_workspace_bytes", "ssd_glr_bwd",
+           "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd_workspace_bytes", "ssd_conv_bwd",
+           "ssd_conv_step", "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd_workspace_bytes",
+           "ssd_norm_bwd",
            "ssd_status_str", "ssd_last_error", "ssd_version"]
 # segsum evaluations of the mask export (ssd.h SSD_SEGSUM_*)
 SEGSUM = {"hierarchy": 0, "direct": 1, "diff": 2}
@@ -127,6 +133,8 @@ def load_library():
     lib.ssd_debug_exp2_probe.restype = i32
     lib.ssd_fwd_noalloc.argtypes = fwd_args[:13] + [vp]
     lib.ssd_fwd_noalloc.restype = i32
+    from . import layer
+    layer.declare(lib)
     lib.ssd_status_str.argtypes = [i32]
     lib.ssd_status_str.restype = ctypes.c_char_p
     lib.ssd_last_error.argtypes = []
@@ -523,3 +531,17 @@ def ssd_bwd(x, dt, A, B, C, D, dy, seq_idx=None, init_states=None, dfinal=None, 
                          stream)
     _check(st)
     return out
+
+
+_LAYER = ("ssd_glr_fwd", "ssd_glr_bwd", "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step",
+          "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd", "GlrShape", "ConvShape", "NormShape")
+
+
+def __getattr__(name):
+    # the layer operators' module imports torch, which this one leaves to its
+    # calls
+    if name in _LAYER:
+        from . import layer
+        value = globals()[name] = getattr(layer, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

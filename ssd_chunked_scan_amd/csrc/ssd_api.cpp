@@ -283,6 +283,13 @@ ssd_status_t make_plan(const ssd_shape_t *s, int64_t chunk, ssd_dtype_t io,
 
 }  // namespace
 
+namespace ssd {
+// The host side of the layer operators (ssd_layer_api.cpp) reports its errors
+// and plans through the same thread-local message and device cache.
+void set_last_error(const char *msg) { g_last_error = msg; }
+int compute_units(hipStream_t stream) { return device_cus(stream); }
+}  // namespace ssd
+
 extern "C" {
 
 const char *ssd_status_str(ssd_status_t status) {
