@@ -70,6 +70,7 @@ struct NormArgs {
     int quant_block;                // 0: the whole group
     int64_t rows;
     int columns, ngroups, width;    // width = columns / ngroups
+    int cus;                        // compute units
     int parts;                      // backward: workgroups along the rows
 };
 

@@ -310,6 +310,7 @@ ssd_status_t norm_fwd(const ssd_norm_shape_t *s, ssd_dtype_t io, const void *x, 
     a.residual_out = residual_out;
     a.y = y;
     a.scales = quant ? scales : nullptr;
+    a.cus = ssd::compute_units((hipStream_t)stream);
     const int n = wide_of(io);
     const int64_t dense = s->columns * (int64_t)e;
     Access acc(a.width % n == 0, n, io);

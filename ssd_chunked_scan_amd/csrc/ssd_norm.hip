@@ -139,6 +139,10 @@ __device__ inline void store_e4m3(uint8_t *p, const float (&y)[V], float inv) {
     }
 }
 
+// As many workgroups as are resident take the rows in turn, the weights in
+// registers and the next row loading while this one is summed and stored:
+// 73 us for 16384 rows of 2560 with the residual (4.6 TB/s; without the row
+// ahead 74 us, a wave per row and five packs a lane 86 us).
 template <typename IO, int V, bool WAVE, int K, int MODE, bool QUANT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormArgs a) {
     constexpr int RPB = WAVE ? 4 : 1;   // rows a workgroup takes at a time
@@ -148,21 +152,40 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormArgs a)
     const int npack = a.width / V;
     const int col0 = g * a.width;
     const float inv_n = 1.f / (float)a.width;
-    for (int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x / 64 : 0); row < a.rows;
-         row += (int64_t)gridDim.x * RPB) {
-        const char *xb = (const char *)a.x + row * a.xs + col0 * (int)sizeof(IO);
-        const char *ob = MODE == kNormResidual ? (const char *)a.residual + row * a.rs + col0 * (int)sizeof(IO)
-                         : MODE == kNormGate   ? (const char *)a.z + row * a.zs + col0 * (int)sizeof(IO)
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x / 64 : 0);
+    Pack<IO, V> xr[K], other[K], xn[K], on[K];
+    auto load = [&](int64_t r, Pack<IO, V> (&x)[K], Pack<IO, V> (&o)[K]) {
+        const char *xb = (const char *)a.x + r * a.xs + col0 * (int)sizeof(IO);
+        const char *ob = MODE == kNormResidual ? (const char *)a.residual + r * a.rs + col0 * (int)sizeof(IO)
+                         : MODE == kNormGate   ? (const char *)a.z + r * a.zs + col0 * (int)sizeof(IO)
                                                : nullptr;
-        Pack<IO, V> xr[K], other[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
             if (p < npack) {
-                xr[k] = load_pack<IO, V>(xb + p * (V * (int)sizeof(IO)));
-                if (MODE != kNormPlain) other[k] = load_pack<IO, V>(ob + p * (V * (int)sizeof(IO)));
+                x[k] = load_pack<IO, V>(xb + p * (V * (int)sizeof(IO)));
+                if (MODE != kNormPlain) o[k] = load_pack<IO, V>(ob + p * (V * (int)sizeof(IO)));
             }
         }
+    };
+    if (row < a.rows) load(row, xr, other);
+    constexpr bool HOLD = K * V <= 8;   // as in the backward kernel
+    float wr[HOLD ? K : 1][HOLD ? V : 1];
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+#pragma unroll
+            for (int v = 0; v < V; ++v) wr[k][v] = p < npack && a.weight ? a.weight[col0 + p * V + v] : 1.f;
+        }
+    }
+    auto weight = [&](int k, int p, int v) {
+        if constexpr (HOLD) return wr[k][v];
+        else return a.weight ? a.weight[col0 + p * V + v] : 1.f;
+    };
+    for (; row < a.rows; row += step) {
+        if (row + step < a.rows) load(row + step, xn, on);
         float val[K][V], ss = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -198,8 +221,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormArgs a)
             if (p < npack) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float w = a.weight ? a.weight[col0 + p * V + v] : 1.f;
-                    val[k][v] = val[k][v] * rstd * w;
+                    val[k][v] = val[k][v] * rstd * weight(k, p, v);
                     if (QUANT) most[k] = max(most[k], abs_bits(val[k][v]));
                 }
                 if (!QUANT) store_pack<IO, V>((IO *)a.y + row * a.columns + col0 + p * V, val[k]);
@@ -240,13 +262,22 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormArgs a)
                 }
             }
         }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            xr[k] = xn[k];
+            other[k] = on[k];
+        }
     }
 }
 
 // Backward: a.parts workgroups per group take the rows in turn and keep their
-// columns' dweight sums in registers; each leaves one row of parts.
+// columns' dweight sums in registers; each leaves one row of parts.  Bound by
+// registers before memory: at most 8 columns a thread (up to 8192 a group),
+// so that two workgroups of ten waves fit a compute unit at 5120 columns
+// (195 us for 16384 gated rows, 4.3 TB/s; 16 columns a thread in half the
+// threads spills: 403 us; loading a row ahead costs one of the two: 199 us).
 template <typename IO, int V, bool WAVE, int K, bool GATE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 5 : 4) void norm_bwd_kernel(NormArgs a) {
     constexpr int RPB = WAVE ? 4 : 1;
     __shared__ float lds[32];
     __shared__ float red[WAVE ? 4 : 1][WAVE ? 64 * K * V : 1];
@@ -256,23 +287,32 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a)
     const int npack = a.width / V;
     const int col0 = g * a.width;
     const float inv_n = 1.f / (float)a.width;
-    float w[K][V], dw[K][V];
+    // the weights in registers too, unless the columns' sums take them all
+    constexpr bool HOLD = K * V <= 8;
+    float wr[HOLD ? K : 1][HOLD ? V : 1], dw[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int p = pack_at<V>(k, tid, nthr);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            w[k][v] = p < npack && a.weight ? a.weight[col0 + p * V + v] : 1.f;
+            if constexpr (HOLD) wr[k][v] = p < npack && a.weight ? a.weight[col0 + p * V + v] : 1.f;
             dw[k][v] = 0.f;
         }
     }
-    for (int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? wave : 0); row < a.rows;
-         row += (int64_t)gridDim.x * RPB) {
-        const char *xb = (const char *)a.x + row * a.xs + col0 * (int)sizeof(IO);
-        const char *db = (const char *)a.dy + row * a.dys + col0 * (int)sizeof(IO);
-        const char *zb = (const char *)a.z + row * a.zs + col0 * (int)sizeof(IO);
-        const char *rb = (const char *)a.dresidual + row * a.drs + col0 * (int)sizeof(IO);
-        Pack<IO, V> xr[K], dr[K], zr[K], rr[K];
+    auto weight = [&](int k, int p, int v) {
+        if constexpr (HOLD) return wr[k][v];
+        else return a.weight ? a.weight[col0 + p * V + v] : 1.f;
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? wave : 0);
+    // third: z with the gate, dresidual without
+    const void *third = GATE ? a.z : a.dresidual;
+    const int64_t ts = GATE ? a.zs : a.drs;
+    Pack<IO, V> xr[K], dr[K], tr[K];
+    auto load = [&](int64_t r) {
+        const char *xb = (const char *)a.x + r * a.xs + col0 * (int)sizeof(IO);
+        const char *db = (const char *)a.dy + r * a.dys + col0 * (int)sizeof(IO);
+        const char *tb = (const char *)third + r * ts + col0 * (int)sizeof(IO);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
@@ -280,24 +320,27 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a)
                 const int off = p * (V * (int)sizeof(IO));
                 xr[k] = load_pack<IO, V>(xb + off);
                 dr[k] = load_pack<IO, V>(db + off);
-                if (GATE) zr[k] = load_pack<IO, V>(zb + off);
-                if (!GATE && a.dresidual) rr[k] = load_pack<IO, V>(rb + off);
+                if (third) tr[k] = load_pack<IO, V>(tb + off);
             }
         }
+    };
+    if (row < a.rows) load(row);
+    for (; row < a.rows; row += step) {
         float val[K][V], ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (pack_at<V>(k, tid, nthr) < npack) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float f = (float)xr[k].v[v];
                     if (GATE) {
-                        const float z = (float)zr[k].v[v];
+                        const float z = (float)tr[k].v[v];
                         f *= z * sigmoid_f32(z);
                     }
                     val[k][v] = f;
                     ss = fmaf(f, f, ss);
-                    sd = fmaf(w[k][v] * (float)dr[k].v[v], f, sd);
+                    sd = fmaf(weight(k, p, v) * (float)dr[k].v[v], f, sd);
                 }
             }
         }
@@ -313,11 +356,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a)
                 for (int v = 0; v < V; ++v) {
                     const float n = val[k][v] * rstd, d = (float)dr[k].v[v];
                     dw[k][v] = fmaf(d, n, dw[k][v]);
-                    float dv = rstd * fmaf(-n, mean, w[k][v] * d);
-                    if (!GATE && a.dresidual) dv += (float)rr[k].v[v];
+                    float dv = rstd * fmaf(-n, mean, weight(k, p, v) * d);
+                    if (!GATE && a.dresidual) dv += (float)tr[k].v[v];
                     dx[v] = dv;
                     if (GATE) {
-                        const float z = (float)zr[k].v[v], s = sigmoid_f32(z);
+                        const float z = (float)tr[k].v[v], s = sigmoid_f32(z);
                         dx[v] = dv * (z * s);
                         dz[v] = dv * (float)xr[k].v[v] * (s * fmaf(z, 1.f - s, 1.f));
                     }
@@ -327,6 +370,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a)
                 if (GATE) store_pack<IO, V>((IO *)a.dz + at, dz);
             }
         }
+        if (row + step < a.rows) load(row + step);
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * a.columns + col0;
@@ -352,7 +396,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormArgs a)
 template <typename IO, int V, bool WAVE, int K>
 static void norm_fwd_launch(const NormArgs &a, hipStream_t stream, int nthr) {
     const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
-    const dim3 grid((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)a.ngroups);
+    const int64_t fit = std::max<int64_t>(1, (int64_t)a.cus * (2048 / nthr) / a.ngroups);
+    const dim3 grid((unsigned)std::min(rows, fit), (unsigned)a.ngroups);
     const int mode = a.residual ? kNormResidual : a.z ? kNormGate : kNormPlain;
 #define SSD_NORM_FWD(M)                                                                                        \
     if (mode == M) {                                                                                           \
@@ -379,42 +424,42 @@ static void norm_bwd_launch(const NormArgs &a, hipStream_t stream, int nthr) {
 // Threads of a workgroup that holds npack packs, K to a thread, in whole waves.
 static int norm_threads(int npack, int K) { return ((npack + K - 1) / K + 63) / 64 * 64; }
 
-// A wave per row and group where it can hold KW packs a lane, but not when
-// there are too few of them to fill the device: then a workgroup each.
-template <typename IO, int V, int KW, int KB>
+// A wave per row and group where it can hold KW packs a lane; a workgroup of
+// KB packs a thread while 1024 threads can hold the group, else of KX.
+template <typename IO, int V, int KW, int KB, int KX>
 static void norm_fwd_shape(const NormArgs &a, hipStream_t stream) {
     const int npack = a.width / V;
-    if (npack <= 64 || (npack <= 64 * KW && a.rows * a.ngroups >= 2048))
+    if (npack <= 64 * KW)
         norm_fwd_launch<IO, V, true, KW>(a, stream, 256);
-    else if (V > 1 || npack <= 8192)
+    else if (npack <= 1024 * KB)
         norm_fwd_launch<IO, V, false, KB>(a, stream, norm_threads(npack, KB));
     else
-        norm_fwd_launch<IO, V, false, V == 1 ? 16 : KB>(a, stream, 1024);
+        norm_fwd_launch<IO, V, false, KX>(a, stream, norm_threads(npack, KX));
 }
 
-template <typename IO, int V, int KW, int KB>
+template <typename IO, int V, int KW, int KB, int KX>
 static void norm_bwd_shape(const NormArgs &a, hipStream_t stream) {
     const int npack = a.width / V;
     if (npack <= 64 * KW)
         norm_bwd_launch<IO, V, true, KW>(a, stream, 256);
-    else if (V > 1 || npack <= 8192)
+    else if (npack <= 1024 * KB)
         norm_bwd_launch<IO, V, false, KB>(a, stream, norm_threads(npack, KB));
     else
-        norm_bwd_launch<IO, V, false, V == 1 ? 16 : KB>(a, stream, 1024);
+        norm_bwd_launch<IO, V, false, KX>(a, stream, norm_threads(npack, KX));
 }
 
 void launch_norm_fwd(bool bf16_io, bool wide, const NormArgs &a, hipStream_t stream) {
     if (bf16_io)
-        wide ? norm_fwd_shape<bf16, 8, 8, 2>(a, stream) : norm_fwd_shape<bf16, 1, 8, 8>(a, stream);
+        wide ? norm_fwd_shape<bf16, 8, 1, 1, 2>(a, stream) : norm_fwd_shape<bf16, 1, 8, 8, 16>(a, stream);
     else
-        wide ? norm_fwd_shape<float, 4, 8, 4>(a, stream) : norm_fwd_shape<float, 1, 8, 8>(a, stream);
+        wide ? norm_fwd_shape<float, 4, 2, 2, 4>(a, stream) : norm_fwd_shape<float, 1, 8, 8, 16>(a, stream);
 }
 
 void launch_norm_bwd(bool bf16_io, bool wide, const NormArgs &a, float *dweight, hipStream_t stream) {
     if (bf16_io)
-        wide ? norm_bwd_shape<bf16, 8, 2, 2>(a, stream) : norm_bwd_shape<bf16, 1, 4, 8>(a, stream);
+        wide ? norm_bwd_shape<bf16, 8, 1, 1, 2>(a, stream) : norm_bwd_shape<bf16, 1, 4, 4, 16>(a, stream);
     else
-        wide ? norm_bwd_shape<float, 4, 4, 4>(a, stream) : norm_bwd_shape<float, 1, 4, 8>(a, stream);
+        wide ? norm_bwd_shape<float, 4, 2, 2, 4>(a, stream) : norm_bwd_shape<float, 1, 4, 4, 16>(a, stream);
     if (dweight) launch_part_sum(a.part, a.parts, a.columns, 1, dweight, nullptr, stream, 1);
 }
 
