@@ -394,7 +394,7 @@ ssd_status_t ssd_glr_fwd(const ssd_glr_shape_t *shape, ssd_dtype_t io,
  * (nullable; only with init_states) [batch][channels], dA, dbias (exactly
  * when bias is given) [channels]: fp32.  Where k_t = 0 its derivative is
  * taken as 0.  Workspace: ssd_glr_bwd_workspace_bytes, 16-byte aligned:
- * 20 bytes per channel, row and 128-token block. */
+ * 20 bytes per channel, row and 64-token block. */
 size_t ssd_glr_bwd_workspace_bytes(const ssd_glr_shape_t *shape, ssd_dtype_t io);
 ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io,
                          const void *x, const void *g, const float *A, const float *bias,

@@ -18,6 +18,8 @@
 // of the round, in registers.
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_layer.hpp"
 
 namespace ssd {
@@ -32,14 +34,18 @@ struct GlrTile {
     static constexpr int CT = CL * V;        // channels per workgroup
 };
 
-// Pairs of channels: a token's strip is 64 (bf16) or 128 (fp32) bytes, so that
-// the strips of a narrow layer still fill the device (5120 channels x 8 rows:
-// 1280 workgroups).  The single-channel tile is for odd widths and strides and
-// for pointers that do not allow pairs.  Both take RT = 128 tokens a round.
-typedef GlrTile<2, 16, 8, 4> GlrPair;
-typedef GlrTile<1, 32, 16, 4> GlrSingle;
-constexpr int kGlrRound = 128;
-static_assert(GlrPair::RT == kGlrRound && GlrSingle::RT == kGlrRound, "one round length");
+// Pairs of channels, 32 lanes of them: a token's strip is a 128-byte line in
+// bf16 (with 64 bytes the forward walk over 8 x 2048 x 5120 took 168 us
+// instead of 155).  The single-channel tiles are for odd widths and strides
+// and for pointers that do not allow pairs.  The backward tiles hold half as
+// many tokens a lane, since seven values of each stay in registers.
+typedef GlrTile<2, 32, 8, 8> GlrFwdPair;
+typedef GlrTile<1, 32, 16, 4> GlrFwdSingle;
+typedef GlrTile<2, 32, 4, 8> GlrBwdPair;
+typedef GlrTile<1, 32, 8, 4> GlrBwdSingle;
+constexpr int kGlrFwdRound = 128, kGlrBwdBlock = 64;   // tokens a forward round, a backward block
+static_assert(GlrFwdPair::RT == kGlrFwdRound && GlrFwdSingle::RT == kGlrFwdRound, "");
+static_assert(GlrBwdPair::RT == kGlrBwdBlock && GlrBwdSingle::RT == kGlrBwdBlock, "");
 
 constexpr float kGlrReset = -0.f;
 __device__ inline bool glr_is_reset(float p) { return __float_as_int(p) < 0; }
@@ -82,20 +88,32 @@ __device__ inline GlrUnit glr_unit(const GlrArgs &a, int nblk) {
     return r;
 }
 
-// A lane's T tokens of a round, token strip `base` (token 0 of the round, byte
-// offset `cb` of its channels); tokens from `valid` on repeat the last one.
-template <typename IO, int V, int T>
-__device__ inline void glr_load(Pack<IO, V> (&r)[T], const char *base, int64_t stride, int m, int cb, int valid) {
-    if (m + T <= valid) {
-        const uint32_t off = (uint32_t)m * (uint32_t)stride + (uint32_t)cb;
+// A lane's T tokens from token m of a run on: `base` is the run's token 0, the
+// same for the whole workgroup, cb the byte offset of the lane's channels.
+// Tokens from `valid` on repeat the last one (not FULL).
+template <bool FULL, typename R, int T>
+__device__ inline void glr_load(R (&r)[T], const char *base, int64_t stride, int m, int cb, int valid) {
+    const __amdgpu_buffer_rsrc_t b = buffer_of(base);
+    const uint32_t st = (uint32_t)stride;
+    if (FULL) {
+        const uint32_t off = (uint32_t)m * st + (uint32_t)cb;
 #pragma unroll
-        for (int i = 0; i < T; ++i) r[i] = load_pack<IO, V>(base + i * stride + off);
+        for (int i = 0; i < T; ++i) r[i] = buffer_load<R>(b, off, i * st);
     } else {
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            const uint32_t tok = (uint32_t)min(m + i, valid - 1);
-            r[i] = load_pack<IO, V>(base + (tok * (uint32_t)stride + (uint32_t)cb));
-        }
+        for (int i = 0; i < T; ++i) r[i] = buffer_load<R>(b, (uint32_t)min(m + i, valid - 1) * st + (uint32_t)cb, 0);
+    }
+}
+
+// The same from the lane's own first token on, `valid` of them.
+template <typename R, int T>
+__device__ inline void glr_load_lane(R (&r)[T], const char *p, int64_t stride, int valid) {
+    if (valid >= T) {
+#pragma unroll
+        for (int i = 0; i < T; ++i, p += stride) r[i] = *(const R *)p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < T; ++i) r[i] = *(const R *)(p + min(i, valid - 1) * stride);
     }
 }
 
@@ -114,14 +132,39 @@ __device__ inline uint32_t glr_resets(const int32_t *seq, int t, int L) {
     return bits;
 }
 
+// h after the maps of the segments before `seg` (wave `wave`'s are TL::TL in a
+// row): whole waves first, so that their maps are read together.
+template <bool PACKED, typename TL>
+__device__ inline void glr_enter(float (&h)[TL::V], const float2 (&maps)[TL::SEG][TL::CT], int ch, int seg) {
+    const int wave = __builtin_amdgcn_readfirstlane(seg / TL::TL), mine = seg % TL::TL;
+#pragma unroll 4
+    for (int s = 0; s < wave * TL::TL; ++s) {
+        float2 f[TL::V];
+#pragma unroll
+        for (int v = 0; v < TL::V; ++v) f[v] = maps[s][ch + v];
+#pragma unroll
+        for (int v = 0; v < TL::V; ++v) h[v] = glr_apply<PACKED>(f[v].x, h[v], f[v].y);
+    }
+#pragma unroll
+    for (int j = 0; j < TL::TL - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < TL::V; ++v) {
+            const float2 f = maps[wave * TL::TL + j][ch + v];
+            const float n = glr_apply<PACKED>(f.x, h[v], f.y);
+            h[v] = j < mine ? n : h[v];
+        }
+}
+
 // The forward walk: one workgroup per (row, split, strip), round after round
 // with the strip's state carried through LDS.  Per round each lane forms the
 // maps of its tokens, publishes its segment's map, and after one barrier
 // composes the segments before its own.  x and g of the next round are loaded
-// meanwhile.
-template <typename IO, typename TL, bool NORM, bool PACKED>
+// as soon as this round's are used up.
+template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
 __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     __shared__ float2 seg_map[2][SEG][CT];
     __shared__ float carry[2][CT];
     const GlrUnit u = glr_unit<TL>(a, a.nblk);
@@ -137,60 +180,80 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
         A[v] = a.A[cc + v];
         bias[v] = a.bias ? a.bias[cc + v] : 0.f;
     }
-    if (seg == SEG - 1) {
-        // the state entering this split: the maps of the splits before it
+    // The state entering this split: the maps of the splits before it.  Every
+    // lane forms it: under a divergent branch the scalar row offsets would be
+    // merged into vector registers, and every address with them.
+    {
+        float h[V];
+        const int64_t at = (int64_t)u.b * a.nblk * D + cc;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float h = a.init ? a.init[(int64_t)u.b * D + cc + v] : 0.f;
-            const int64_t at = (int64_t)u.b * a.nblk * D + cc + v;
-            for (int q = 0; q < u.blk; ++q) 
-                h = glr_apply<PACKED>(a.ws_p[at + (int64_t)q * D], h, a.ws_h[at + (int64_t)q * D]);
-            carry[0][cg * V + v] = h;
+        for (int v = 0; v < V; ++v) h[v] = a.init ? a.init[(int64_t)u.b * D + cc + v] : 0.f;
+        for (int s = 0; s < u.blk; s += 8) {
+            float p[8][V], q[8][V];   // eight at a time: one wait for their loads
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int64_t k = at + (int64_t)min(s + j, u.blk - 1) * D + v;
+                    p[j][v] = a.ws_p[k];
+                    q[j][v] = a.ws_h[k];
+                }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (s + j < u.blk) h[v] = glr_apply<PACKED>(p[j][v], h[v], q[j][v]);
         }
+        if (seg == SEG - 1)
+#pragma unroll
+            for (int v = 0; v < V; ++v) carry[0][cg * V + v] = h[v];
     }
     const int cb = cc * (int)sizeof(IO);
     const int64_t row = (int64_t)u.b * L;
     const char *xb = (const char *)a.x + row * a.xs;
     const char *gb = (const char *)a.g + row * a.gs;
     const char *zb = (const char *)a.z + row * a.zs;
-    IO *yb = (IO *)a.y + row * D;
-    Pack<IO, V> xr[T], gr[T], xn[T], gn[T], zr[T];
-    glr_load<IO, V, T>(xr, xb + t0 * a.xs, a.xs, m, cb, L - t0);
-    glr_load<IO, V, T>(gr, gb + t0 * a.gs, a.gs, m, cb, L - t0);
-    int buf = 0;
-    for (int t = t0; t < t1; t += TL::RT, buf ^= 1) {
-        if (a.z) glr_load<IO, V, T>(zr, zb + t * a.zs, a.zs, m, cb, L - t);
-        if (t + TL::RT < t1) {
-            glr_load<IO, V, T>(xn, xb + (t + TL::RT) * a.xs, a.xs, m, cb, L - t - TL::RT);
-            glr_load<IO, V, T>(gn, gb + (t + TL::RT) * a.gs, a.gs, m, cb, L - t - TL::RT);
+    char *yb = (char *)a.y + row * D * (int)sizeof(IO);
+    const int64_t ys = (int64_t)D * (int)sizeof(IO);
+    R xr[T], gr[T], zr[T];
+    auto load = [&](int t) {
+        if (t + TL::RT <= L) {
+            glr_load<true>(xr, xb + t * a.xs, a.xs, m, cb, 0);
+            glr_load<true>(gr, gb + t * a.gs, a.gs, m, cb, 0);
+        } else {
+            glr_load<false>(xr, xb + t * a.xs, a.xs, m, cb, L - t);
+            glr_load<false>(gr, gb + t * a.gs, a.gs, m, cb, L - t);
         }
+    };
+    auto round = [&](int t, int buf, auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t + m, L) : 0u;
         float p[T][V], q[T][V];
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int i = 0; i < T; ++i) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float k;
-                gate_map<NORM>((float)gr[i].v[v] + bias[v], A[v], p[i][v], k);
-                q[i][v] = k * (float)xr[i].v[v];
-            }
-        if (PACKED) {
-            const uint32_t cut = glr_resets<T>(a.seq_idx + row, t + m, L);
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) p[i][v] = glr_mark<PACKED>(p[i][v], (cut >> i) & 1);
-        }
-        if (t + m + T > L) {
-            // past the row's end: the identity map
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
+                gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p[i][v], k);
+                p[i][v] = glr_mark<PACKED>(p[i][v], (cut >> i) & 1);
+                q[i][v] = k * RW::at(xr[i], v);
+                if (!FULL) {
+                    // past the row's end: the identity map
                     const bool ok = t + m + i < L;
                     p[i][v] = ok ? p[i][v] : 1.f;
                     q[i][v] = ok ? q[i][v] : 0.f;
                 }
+            }
         }
+        // the maps are formed here, before the next loads take the registers of
+        // the words they came from, and not sunk to their use behind them
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(p[i][v]), "+v"(q[i][v]));
+        // (z in front of them: waiting for it does not wait for them)
+        if (GATE) glr_load<FULL>(zr, zb + t * a.zs, a.zs, m, cb, L - t);
+        if (t + TL::RT < t1) load(t + TL::RT);
         float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -205,12 +268,9 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = carry[buf][cg * V + v];
-        for (int s = 0; s < seg; ++s)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 f = seg_map[buf][s][cg * V + v];
-                h[v] = glr_apply<PACKED>(f.x, h[v], f.y);
-            }
+        glr_enter<PACKED, TL>(h, seg_map[buf], cg * V, seg);
+        const __amdgpu_buffer_rsrc_t yt = buffer_of(yb + t * ys);
+        const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             float o[V];
@@ -218,15 +278,12 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
             for (int v = 0; v < V; ++v) {
                 h[v] = glr_apply<PACKED>(p[i][v], h[v], q[i][v]);
                 o[v] = h[v];
-            }
-            if (a.z) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float z = (float)zr[i].v[v];
+                if (GATE) {
+                    const float z = RW::at(zr[i], v);
                     o[v] *= z * sigmoid_f32(z);
                 }
             }
-            if (cok && t + m + i < L) store_pack<IO, V>(yb + (int64_t)(t + m + i) * D + cc, o);
+            if (FULL || (cok && t + m + i < L)) buffer_store<IO, V>(yt, off, (uint32_t)(i * ys), o);
         }
         if (seg == SEG - 1) {
 #pragma unroll
@@ -235,12 +292,14 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
                 if (t + TL::RT >= L && a.final_states && cok) a.final_states[(int64_t)u.b * D + cc + v] = h[v];
             }
         }
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-            xr[i] = xn[i];
-            gr[i] = gn[i];
-        }
-    }
+    };
+    load(t0);
+    // whole rounds of a whole strip in a loop of their own: the guarded form
+    // beside them would take half as many registers again
+    int buf = 0, t = t0;
+    if ((u.ct + 1) * CT <= D)
+        for (; t < t1 && t + TL::RT <= L; t += TL::RT, buf ^= 1) round(t, buf, std::true_type{});
+    for (; t < t1; t += TL::RT, buf ^= 1) round(t, buf, std::false_type{});
 }
 
 // The map of each block of blk_len tokens (ws_p, ws_h), and with BWD the
@@ -248,9 +307,11 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
 // with G_t = e_t + c_t and c_{t-1} = p_t G_t, c before the block is
 // sum_t (p_first .. p_t) e_t.  Each lane walks its segment of blk_len / SEG
 // tokens; the segments are joined at the end.
-template <typename IO, typename TL, bool NORM, bool PACKED, bool BWD>
+template <typename IO, typename TL, bool NORM, bool PACKED, bool BWD, bool GATE>
 __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nblk) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     __shared__ float2 seg_map[SEG][CT];
     __shared__ float seg_e[BWD ? SEG : 1][CT];
     const GlrUnit u = glr_unit<TL>(a, nblk);
@@ -279,11 +340,11 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
         // times the stride can pass 32 bits
         const int t = t0 + seg * per + j;
         if (t >= L) break;   // no barrier inside the loop
-        Pack<IO, V> xr[T], gr[T], zr[T], dr[T];
-        glr_load<IO, V, T>(xr, xb + t * a.xs, a.xs, 0, cb, L - t);
-        glr_load<IO, V, T>(gr, gb + t * a.gs, a.gs, 0, cb, L - t);
-        if (BWD) glr_load<IO, V, T>(dr, db + t * a.dys, a.dys, 0, cb, L - t);
-        if (BWD && a.z) glr_load<IO, V, T>(zr, zb + t * a.zs, a.zs, 0, cb, L - t);
+        R xr[T], gr[T], zr[T], dr[T];
+        glr_load_lane(xr, xb + t * a.xs + cb, a.xs, L - t);
+        glr_load_lane(gr, gb + t * a.gs + cb, a.gs, L - t);
+        if (BWD) glr_load_lane(dr, db + t * a.dys + cb, a.dys, L - t);
+        if (BWD && GATE) glr_load_lane(zr, zb + t * a.zs + cb, a.zs, L - t);
         const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t, L) : 0u;
 #pragma unroll
         for (int i = 0; i < T; ++i) {
@@ -291,15 +352,15 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float p, k;
-                gate_map<NORM>((float)gr[i].v[v] + bias[v], A[v], p, k);
-                const float q = ok ? k * (float)xr[i].v[v] : 0.f;
+                gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p, k);
+                const float q = ok ? k * RW::at(xr[i], v) : 0.f;
                 p = ok ? glr_mark<PACKED>(p, (cut >> i) & 1) : 1.f;
                 qs[v] = glr_apply<PACKED>(p, qs[v], q);
                 ps[v] = glr_join<PACKED>(ps[v], p);
                 if (BWD) {
-                    float e = (float)dr[i].v[v];
-                    if (a.z) {
-                        const float z = (float)zr[i].v[v];
+                    float e = RW::at(dr[i], v);
+                    if (GATE) {
+                        const float z = RW::at(zr[i], v);
                         e *= z * sigmoid_f32(z);
                     }
                     es[v] = glr_apply<PACKED>(ps[v], ok ? e : 0.f, es[v]);
@@ -335,9 +396,11 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
 //   dx = k G     dla = c_{t-1} h_{t-1} + G x dk/dla,  dk/dla = -a^2 / k
 //   dg = A dla sigmoid(g + bias)   dA = sum s dla   dbias = sum dg
 //   dz = dy h silu'(z)
-template <typename IO, typename TL, bool NORM, bool PACKED>
-__global__ __launch_bounds__(TL::W * 64) void glr_bwd_kernel(GlrArgs a) {
+template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
+__global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel(GlrArgs a) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     __shared__ float2 seg_map[SEG][CT];
     __shared__ float seg_e[SEG][CT];
     const GlrUnit u = glr_unit<TL>(a, a.nblk);
@@ -349,113 +412,123 @@ __global__ __launch_bounds__(TL::W * 64) void glr_bwd_kernel(GlrArgs a) {
     const int t = u.blk * TL::RT;
     const int64_t row = (int64_t)u.b * L;
     const int64_t wsat = ((int64_t)u.b * a.nblk + u.blk) * D + cc;
-    Pack<IO, V> xr[T], gr[T], zr[T], dr[T];
-    glr_load<IO, V, T>(gr, (const char *)a.g + (row + t) * a.gs, a.gs, m, cb, L - t);
-    glr_load<IO, V, T>(xr, (const char *)a.x + (row + t) * a.xs, a.xs, m, cb, L - t);
-    glr_load<IO, V, T>(dr, (const char *)a.dy + (row + t) * a.dys, a.dys, m, cb, L - t);
-    if (a.z) glr_load<IO, V, T>(zr, (const char *)a.z + (row + t) * a.zs, a.zs, m, cb, L - t);
-    const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t + m, L) : 0u;
-    float A[V], bias[V], hin[V], cin[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = a.A[cc + v];
-        bias[v] = a.bias ? a.bias[cc + v] : 0.f;
-        hin[v] = a.ws_h[wsat + v];
-        cin[v] = a.ws_e[wsat + v];
-    }
-    float al[T][V], k[T][V], sp[T][V], sg[T][V], sz[T][V];
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-        const bool ok = t + m + i < L;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float gv = (float)gr[i].v[v] + bias[v];
-            float e, w;
-            const float s = softplus_precise(gv, e, w), la = A[v] * s;
-            const float av = __builtin_amdgcn_exp2f(kLog2e * la);
-            al[i][v] = ok ? av : 1.f;
-            k[i][v] = ok ? (NORM ? __builtin_amdgcn_sqrtf(one_minus_square(av, la)) : 1.f) : 0.f;
-            sp[i][v] = ok ? s : 0.f;
-            sg[i][v] = ok ? (gv >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(w) : 0.f;
-            sz[i][v] = a.z ? sigmoid_f32((float)zr[i].v[v]) : 0.f;
-        }
-    }
-    auto p_of = [&](int i, int v) { return glr_mark<PACKED>(al[i][v], (cut >> i) & 1); };
-    auto e_of = [&](int i, int v) {
-        const float d = (float)dr[i].v[v];
-        const float e = a.z ? d * ((float)zr[i].v[v] * sz[i][v]) : d;
-        return t + m + i < L ? e : 0.f;
-    };
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float ps = 1.f, qs = 0.f, es = 0.f;
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-            const float p = p_of(i, v);
-            qs = glr_apply<PACKED>(p, qs, k[i][v] * (float)xr[i].v[v]);
-            ps = glr_join<PACKED>(ps, p);
-            es = glr_apply<PACKED>(ps, e_of(i, v), es);
-        }
-        seg_map[seg][cg * V + v] = make_float2(ps, qs);
-        seg_e[seg][cg * V + v] = es;
-    }
-    __syncthreads();
-    for (int s = 0; s < seg; ++s)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float2 f = seg_map[s][cg * V + v];
-            hin[v] = glr_apply<PACKED>(f.x, hin[v], f.y);
-        }
-    for (int s = SEG - 1; s > seg; --s)
-#pragma unroll
-        for (int v = 0; v < V; ++v) 
-            cin[v] = glr_apply<PACKED>(seg_map[s][cg * V + v].x, cin[v], seg_e[s][cg * V + v]);
-    float h[T][V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float hv = hin[v];
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-            hv = glr_apply<PACKED>(p_of(i, v), hv, k[i][v] * (float)xr[i].v[v]);
-            h[i][v] = hv;
-        }
-    }
+    const int64_t ys = (int64_t)D * (int)sizeof(IO);
+    const char *gb = (const char *)a.g + (row + t) * a.gs, *xb = (const char *)a.x + (row + t) * a.xs;
+    const char *db = (const char *)a.dy + (row + t) * a.dys, *zb = (const char *)a.z + (row + t) * a.zs;
     float dA[V], dbias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) dA[v] = dbias[v] = 0.f;
-#pragma unroll
-    for (int i = T - 1; i >= 0; --i) {
-        float dx[V], dg[V], dz[V];
+    auto block = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        R xr[T], gr[T], zr[T], dr[T];
+        glr_load<FULL>(gr, gb, a.gs, m, cb, L - t);
+        glr_load<FULL>(xr, xb, a.xs, m, cb, L - t);
+        glr_load<FULL>(dr, db, a.dys, m, cb, L - t);
+        if (GATE) glr_load<FULL>(zr, zb, a.zs, m, cb, L - t);
+        const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t + m, L) : 0u;
+        float A[V], bias[V], hin[V], cin[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float G = e_of(i, v) + cin[v];
-            const float x = (float)xr[i].v[v];
-            const bool reset = PACKED && ((cut >> i) & 1);
-            cin[v] = reset ? 0.f : al[i][v] * G;
-            dx[v] = k[i][v] * G;
-            float dla = reset ? 0.f : cin[v] * (i > 0 ? h[i > 0 ? i - 1 : 0][v] : hin[v]);
-            if (NORM) {
-                const float rk = k[i][v] > 0.f ? __builtin_amdgcn_rcpf(k[i][v]) : 0.f;
-                dla = fmaf(-G * x, al[i][v] * al[i][v] * rk, dla);
+            A[v] = a.A[cc + v];
+            bias[v] = a.bias ? a.bias[cc + v] : 0.f;
+            hin[v] = a.ws_h[wsat + v];
+            cin[v] = a.ws_e[wsat + v];
+        }
+        auto ok = [&](int i) { return FULL || t + m + i < L; };
+        // decay, input factor, softplus (base 2) and its derivative, the
+        // gate's sigmoid; past the row's end the identity
+        float al[T][V], k[T][V], sp[T][V], sg[T][V], sz[T][V];
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float gv = RW::at(gr[i], v) + bias[v];
+                float e, o;
+                const float s = softplus2(gv, e, o), l = A[v] * s;
+                const float av = __builtin_amdgcn_exp2f(l);
+                al[i][v] = ok(i) ? av : 1.f;
+                k[i][v] = ok(i) ? (NORM ? __builtin_amdgcn_sqrtf(one_minus_square(av, l)) : 1.f) : 0.f;
+                sp[i][v] = ok(i) ? s : 0.f;
+                sg[i][v] = ok(i) ? (gv >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(o) : 0.f;
+                if (GATE) sz[i][v] = sigmoid_f32(RW::at(zr[i], v));
             }
-            dg[v] = A[v] * dla * sg[i][v];
-            dA[v] = fmaf(sp[i][v], dla, dA[v]);
-            dbias[v] += dg[v];
-            const float z = (float)zr[i].v[v];
-            dz[v] = a.z ? (float)dr[i].v[v] * h[i][v] * (sz[i][v] * fmaf(z, 1.f - sz[i][v], 1.f)) : 0.f;
+        auto p_of = [&](int i, int v) { return glr_mark<PACKED>(al[i][v], (cut >> i) & 1); };
+        auto e_of = [&](int i, int v) {
+            const float d = RW::at(dr[i], v);
+            const float e = GATE ? d * (RW::at(zr[i], v) * sz[i][v]) : d;
+            return ok(i) ? e : 0.f;
+        };
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float ps = 1.f, qs = 0.f, es = 0.f;
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                const float p = p_of(i, v);
+                qs = glr_apply<PACKED>(p, qs, k[i][v] * RW::at(xr[i], v));
+                ps = glr_join<PACKED>(ps, p);
+                es = glr_apply<PACKED>(ps, e_of(i, v), es);
+            }
+            seg_map[seg][cg * V + v] = make_float2(ps, qs);
+            seg_e[seg][cg * V + v] = es;
         }
-        if (cok && t + m + i < L) {
-            const int64_t at = (row + t + m + i) * D + cc;
-            store_pack<IO, V>((IO *)a.dx + at, dx);
-            store_pack<IO, V>((IO *)a.dg + at, dg);
-            if (a.z) store_pack<IO, V>((IO *)a.dz + at, dz);
+        __syncthreads();
+        glr_enter<PACKED, TL>(hin, seg_map, cg * V, seg);
+        for (int s = SEG - 1; s > seg; --s)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                cin[v] = glr_apply<PACKED>(seg_map[s][cg * V + v].x, cin[v], seg_e[s][cg * V + v]);
+        float h[T][V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float hv = hin[v];
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                hv = glr_apply<PACKED>(p_of(i, v), hv, k[i][v] * RW::at(xr[i], v));
+                h[i][v] = hv;
+            }
+            dA[v] = dbias[v] = 0.f;
         }
-    }
+        const __amdgpu_buffer_rsrc_t ox = buffer_of((char *)a.dx + (row + t) * ys);
+        const __amdgpu_buffer_rsrc_t og = buffer_of((char *)a.dg + (row + t) * ys);
+        const __amdgpu_buffer_rsrc_t oz = buffer_of((char *)a.dz + (row + t) * ys);
+        const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
+#pragma unroll
+        for (int i = T - 1; i >= 0; --i) {
+            float dx[V], dg[V], dz[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float G = e_of(i, v) + cin[v];
+                const float x = RW::at(xr[i], v);
+                const bool reset = PACKED && ((cut >> i) & 1);
+                cin[v] = reset ? 0.f : al[i][v] * G;
+                dx[v] = k[i][v] * G;
+                float dla = reset ? 0.f : cin[v] * (i > 0 ? h[i > 0 ? i - 1 : 0][v] : hin[v]);
+                if (NORM) {
+                    const float rk = k[i][v] > 0.f ? __builtin_amdgcn_rcpf(k[i][v]) : 0.f;
+                    dla = fmaf(-G * x, al[i][v] * al[i][v] * rk, dla);
+                }
+                dg[v] = A[v] * dla * sg[i][v];
+                dA[v] = fmaf(sp[i][v], dla, dA[v]);
+                dbias[v] += dg[v];
+                if (GATE) {
+                    const float z = RW::at(zr[i], v);
+                    dz[v] = RW::at(dr[i], v) * h[i][v] * (sz[i][v] * fmaf(z, 1.f - sz[i][v], 1.f));
+                }
+            }
+            if (FULL || (cok && ok(i))) {
+                buffer_store<IO, V>(ox, off, (uint32_t)(i * ys), dx);
+                buffer_store<IO, V>(og, off, (uint32_t)(i * ys), dg);
+                if (GATE) buffer_store<IO, V>(oz, off, (uint32_t)(i * ys), dz);
+            }
+        }
+    };
+    if ((u.ct + 1) * CT <= D && t + TL::RT <= L)
+        block(std::true_type{});
+    else
+        block(std::false_type{});
     // dA and dbias of the block: the lanes' sums over their tokens, joined in
     // segment order
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; ++v) seg_map[seg][cg * V + v] = make_float2(dA[v], dbias[v]);
+    for (int v = 0; v < V; ++v) seg_map[seg][cg * V + v] = make_float2(dA[v] * kLn2, dbias[v]);
     __syncthreads();
     if (tid < CT && u.ct * CT + tid < D) {
         float2 s = make_float2(0.f, 0.f);
@@ -481,10 +554,14 @@ inline dim3 glr_grid(const GlrArgs &a, int nblk) {
 
 template <typename IO, typename TL, bool NORM, bool PACKED>
 void launch_glr_fwd_docs(const GlrArgs &a, hipStream_t stream) {
+    const dim3 block(TL::W * 64);
     if (a.nblk > 1)
-        hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, false>), glr_grid<TL>(a, a.nblk - 1),
-                           dim3(TL::W * 64), 0, stream, a, a.nblk - 1);
-    hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, NORM, PACKED>), glr_grid<TL>(a, a.nblk), dim3(TL::W * 64), 0, stream, a);
+        hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, false, false>), glr_grid<TL>(a, a.nblk - 1), block,
+                           0, stream, a, a.nblk - 1);
+    if (a.z)
+        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, NORM, PACKED, true>), glr_grid<TL>(a, a.nblk), block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, NORM, PACKED, false>), glr_grid<TL>(a, a.nblk), block, 0, stream, a);
 }
 
 template <typename IO, typename TL, bool NORM>
@@ -494,12 +571,18 @@ void launch_glr_fwd_tile(const GlrArgs &a, hipStream_t stream) {
 
 void launch_glr_block_scan(const GlrArgs &a, hipStream_t stream);
 
+template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
+void launch_glr_bwd_gate(const GlrArgs &a, hipStream_t stream) {
+    const dim3 grid = glr_grid<TL>(a, a.nblk), block(TL::W * 64);
+    hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, true, GATE>), grid, block, 0, stream, a, a.nblk);
+    launch_glr_block_scan(a, stream);
+    hipLaunchKernelGGL((glr_bwd_kernel<IO, TL, NORM, PACKED, GATE>), grid, block, 0, stream, a);
+}
+
 template <typename IO, typename TL, bool NORM, bool PACKED>
 void launch_glr_bwd_docs(const GlrArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, true>), glr_grid<TL>(a, a.nblk), dim3(TL::W * 64), 0,
-                       stream, a, a.nblk);
-    launch_glr_block_scan(a, stream);
-    hipLaunchKernelGGL((glr_bwd_kernel<IO, TL, NORM, PACKED>), glr_grid<TL>(a, a.nblk), dim3(TL::W * 64), 0, stream, a);
+    a.z ? launch_glr_bwd_gate<IO, TL, NORM, PACKED, true>(a, stream)
+        : launch_glr_bwd_gate<IO, TL, NORM, PACKED, false>(a, stream);
 }
 
 template <typename IO, typename TL, bool NORM>
@@ -511,20 +594,20 @@ void launch_glr_bwd_tile(const GlrArgs &a, hipStream_t stream) {
     template <>                                                                                      \
     void launch_glr_fwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                    \
         if (pair)                                                                                    \
-            a.normalize ? launch_glr_fwd_tile<IO, GlrPair, true>(a, stream)                          \
-                        : launch_glr_fwd_tile<IO, GlrPair, false>(a, stream);                        \
+            a.normalize ? launch_glr_fwd_tile<IO, GlrFwdPair, true>(a, stream)                          \
+                        : launch_glr_fwd_tile<IO, GlrFwdPair, false>(a, stream);                        \
         else                                                                                         \
-            a.normalize ? launch_glr_fwd_tile<IO, GlrSingle, true>(a, stream)                        \
-                        : launch_glr_fwd_tile<IO, GlrSingle, false>(a, stream);                      \
+            a.normalize ? launch_glr_fwd_tile<IO, GlrFwdSingle, true>(a, stream)                        \
+                        : launch_glr_fwd_tile<IO, GlrFwdSingle, false>(a, stream);                      \
     }                                                                                                \
     template <>                                                                                      \
     void launch_glr_bwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                    \
         if (pair)                                                                                    \
-            a.normalize ? launch_glr_bwd_tile<IO, GlrPair, true>(a, stream)                          \
-                        : launch_glr_bwd_tile<IO, GlrPair, false>(a, stream);                        \
+            a.normalize ? launch_glr_bwd_tile<IO, GlrBwdPair, true>(a, stream)                          \
+                        : launch_glr_bwd_tile<IO, GlrBwdPair, false>(a, stream);                        \
         else                                                                                         \
-            a.normalize ? launch_glr_bwd_tile<IO, GlrSingle, true>(a, stream)                        \
-                        : launch_glr_bwd_tile<IO, GlrSingle, false>(a, stream);                      \
+            a.normalize ? launch_glr_bwd_tile<IO, GlrBwdSingle, true>(a, stream)                        \
+                        : launch_glr_bwd_tile<IO, GlrBwdSingle, false>(a, stream);                      \
     }
 
 }  // namespace ssd

@@ -94,43 +94,93 @@ __device__ inline void store_pack(void *p, const float (&f)[V]) {
     *(Pack<IO, V> *)p = o;
 }
 
+// The same kept as one machine word or vector of words, so that what waits in
+// registers takes V * sizeof(IO) bytes; at(r, v) is element v.
+template <int BYTES>
+struct Words;
+template <>
+struct Words<2> { typedef uint16_t type; };
+template <>
+struct Words<4> { typedef uint32_t type; };
+template <>
+struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+
+template <typename IO, int V>
+struct Raw {
+    typedef typename Words<sizeof(IO) * V>::type type;
+    static __device__ inline float at(type r, int v) {
+        if constexpr (sizeof(IO) * V == 2) return __uint_as_float((uint32_t)r << 16);
+        else if constexpr (sizeof(IO) == 4 && V == 1) return __uint_as_float(r);
+        else if constexpr (sizeof(IO) == 4) return __uint_as_float(r[v]);
+        else return __uint_as_float(v ? r & 0xffff0000u : r << 16);
+    }
+};
+
+// Loads and stores through a buffer descriptor: the run's base in scalar
+// registers, a 32-bit offset per lane and a scalar one per token, so that no
+// lane forms a 64-bit address.  Every offset is kept inside the tensor by the
+// caller; the descriptor's own bound is not used.
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, 0xffffffff, 0x00027000);
+}
+
+template <typename R>
+__device__ inline R buffer_load(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t token) {
+    if constexpr (sizeof(R) == 2) return __builtin_amdgcn_raw_buffer_load_b16(b, lane, token, 0);
+    else if constexpr (sizeof(R) == 4) return __builtin_amdgcn_raw_buffer_load_b32(b, lane, token, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b64(b, lane, token, 0);
+}
+
+template <typename IO, int V>
+__device__ inline void buffer_store(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t token, const float (&f)[V]) {
+    typedef typename Words<sizeof(IO) * V>::type R;
+    typedef float fv __attribute__((ext_vector_type(V)));
+    typedef IO iv __attribute__((ext_vector_type(V)));
+    const R r = __builtin_bit_cast(R, __builtin_convertvector(__builtin_bit_cast(fv, f), iv));
+    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(r, b, lane, token, 0);
+    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(r, b, lane, token, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(r, b, lane, token, 0);
+}
+
 // ------------------------------------------------------------------- maps
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in [0, 1].  1 + e is
-// rounded to w and loses c = e - (w - 1), so log(1 + e) = log(w) + c / w up
-// to c^2; 1 / w is only needed to a few bits there, and 1 - e / 2 equals it
-// at both ends.  Keeps the relative accuracy for very negative v, where the
-// decay's distance from 1 is all that matters.  e and w are handed out for
-// the derivative 1 / (1 + exp(-v)) = (v >= 0 ? 1 : e) / w.
-__device__ inline float softplus_precise(float v, float &e, float &w) {
-    e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
-    w = 1.f + e;
-    const float c = e - (w - 1.f);
-    return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, c * fmaf(-0.5f, e, 1.f));
+// The gate's softplus in base-2 units: softplus2(v) = log2(1 + exp(v)) =
+// max(w, 0) + log2(1 + e) with w = v log2(e), e = 2^-|w| in [0, 1].  1 + e is
+// rounded to o and loses c = e - (o - 1), so log2(1 + e) = log2(o) + c log2(e)
+// / o up to c^2; 1 / o is only needed to a few bits there, and 1 - e / 2
+// equals it at both ends.  Keeps the relative accuracy for very negative v,
+// where the decay's distance from 1 is all that matters.  e and o are handed
+// out for the derivative 1 / (1 + exp(-v)) = (v >= 0 ? 1 : e) / o.
+__device__ inline float softplus2(float v, float &e, float &o) {
+    const float w = kLog2e * v;
+    e = __builtin_amdgcn_exp2f(-fabsf(w));
+    o = 1.f + e;
+    const float c = e - (o - 1.f);
+    return fmaxf(w, 0.f) + fmaf(c, fmaf(-0.5f * kLog2e, e, kLog2e), __builtin_amdgcn_logf(o));
 }
 
-// 1 - a^2 for a = exp(la), la <= 0: by the series of 1 - exp(-q), q = -2 la,
+// 1 - a^2 for a = 2^l, l <= 0: by the series of 1 - exp(-q), q = -2 ln(2) l,
 // where a^2 is near 1 (six terms, below 5e-8 relative at q = 1/4), else
 // directly (no more than 2.3 roundings of a^2 lost there).
-__device__ inline float one_minus_square(float a, float la) {
-    const float q = -2.f * la;
-    float p = fmaf(q, -1.f / 720.f, 1.f / 120.f);
-    p = fmaf(q, p, -1.f / 24.f);
-    p = fmaf(q, p, 1.f / 6.f);
-    p = fmaf(q, p, -0.5f);
-    p = fmaf(q, p, 1.f);
-    return q < 0.25f ? q * p : fmaf(-a, a, 1.f);
+__device__ inline float one_minus_square(float a, float l) {
+    constexpr double s = -2.0 * 0.69314718055994530942;
+    float p = fmaf(l, (float)(-s * s * s * s * s * s / 720.), (float)(s * s * s * s * s / 120.));
+    p = fmaf(l, p, (float)(-s * s * s * s / 24.));
+    p = fmaf(l, p, (float)(s * s * s / 6.));
+    p = fmaf(l, p, (float)(-s * s / 2.));
+    p = fmaf(l, p, (float)s);
+    return l > (float)(0.25 / s) ? l * p : fmaf(-a, a, 1.f);
 }
 
 // Decay and input factor of one element.
 template <bool NORM>
 __device__ inline void gate_map(float v, float A, float &a, float &k) {
-    float e, w;
-    const float la = A * softplus_precise(v, e, w);
-    a = __builtin_amdgcn_exp2f(kLog2e * la);
-    k = NORM ? __builtin_amdgcn_sqrtf(one_minus_square(a, la)) : 1.f;
+    float e, o;
+    const float l = A * softplus2(v, e, o);
+    a = __builtin_amdgcn_exp2f(l);
+    k = NORM ? __builtin_amdgcn_sqrtf(one_minus_square(a, l)) : 1.f;
 }
 
 __device__ inline float sigmoid_f32(float z) {

@@ -44,7 +44,7 @@ constexpr int64_t kMaxChannels = (int64_t)1 << 20;   // also of a stride
 constexpr int64_t kMaxThreads = 0xffffffff;          // of one launch
 constexpr int64_t kMaxGrid = kMaxThreads / 256;      // workgroups of 256 threads
 constexpr int64_t kMaxNormWidth = 16384;             // columns of a norm group: held in registers
-constexpr int kRound = 128;                          // tokens per round of the recurrence's kernels
+constexpr int kRound = 128, kBlock = 64;             // tokens per round and per backward block of the recurrence
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -139,22 +139,22 @@ ssd_status_t check_glr(const ssd_glr_shape_t *s, ssd_dtype_t io) {
         return fail(SSD_ERR_UNSUPPORTED, "normalize must be 0 or 1, got %lld", (long long)s->normalize);
     SSD_TRY(check_reserved(s->reserved));
     // the smallest strip is 32 channels
-    const int64_t units = s->batch * ((s->seqlen + kRound - 1) / kRound) * ((s->channels + 31) / 32);
+    const int64_t units = s->batch * ((s->seqlen + kBlock - 1) / kBlock) * ((s->channels + 31) / 32);
     // (the block scan takes 1024 threads for every 64 channels of a row)
     if (units > kMaxGrid || s->batch * ((s->channels + 63) / 64) > kMaxThreads / 1024)
         return fail(SSD_ERR_UNSUPPORTED, "problem too large: %lld work units", (long long)units);
     return SSD_OK;
 }
 
-// Sequence splits of the forward walk: none when rows and strips of 32
+// Sequence splits of the forward walk: none when rows and strips of 64
 // channels give the device work enough; else as many as do, each of at least
 // two rounds.  A split costs a second reading of x and g.
 void glr_fwd_split(const ssd_glr_shape_t *s, hipStream_t stream, int *nblk, int *blk_len) {
     const int64_t rounds = (s->seqlen + kRound - 1) / kRound;
-    const int64_t units = s->batch * ((s->channels + 31) / 32);
+    const int64_t units = s->batch * ((s->channels + 63) / 64);
     const int64_t cus = ssd::compute_units(stream);
     int64_t n = 1;
-    if (units < 2 * cus) n = std::max<int64_t>(1, std::min<int64_t>((3 * cus + units - 1) / units, rounds / 2));
+    if (units < cus) n = std::max<int64_t>(1, std::min<int64_t>((2 * cus + units - 1) / units, rounds / 2));
     const int64_t per = (rounds + n - 1) / n;
     *nblk = (int)((rounds + per - 1) / per);
     *blk_len = (int)(per * kRound);
@@ -165,7 +165,7 @@ size_t glr_fwd_bytes(const ssd_glr_shape_t *s, int nblk) {
 }
 
 size_t glr_bwd_bytes(const ssd_glr_shape_t *s) {
-    const size_t one = sizeof(float) * (size_t)s->batch * ((s->seqlen + kRound - 1) / kRound) * s->channels;
+    const size_t one = sizeof(float) * (size_t)s->batch * ((s->seqlen + kBlock - 1) / kBlock) * s->channels;
     return 3 * round_up(one, 256) + round_up(2 * one, 256);
 }
 
@@ -393,8 +393,8 @@ ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     const size_t bytes = glr_bwd_bytes(shape);
     SSD_TRY(check_workspace(workspace, workspace_bytes, bytes));
     ssd::GlrArgs a = glr_args(shape, io, x, g, A, bias, z, seq_idx, init_states);
-    a.nblk = (int)((shape->seqlen + kRound - 1) / kRound);
-    a.blk_len = kRound;
+    a.nblk = (int)((shape->seqlen + kBlock - 1) / kBlock);
+    a.blk_len = kBlock;
     a.dy = dy;
     a.dfinal = dfinal;
     a.dx = dx;
