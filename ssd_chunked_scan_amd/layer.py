@@ -17,6 +17,8 @@ from typing import Optional, Tuple
 
 import torch
 
+import ssd_chunked_scan_amd as ssd
+
 _I64, _VP = ctypes.c_int64, ctypes.c_void_p
 
 
@@ -53,11 +55,6 @@ def declare(lib) -> None:
             size.restype = sz
 
 
-def _binding():
-    import ssd_chunked_scan_amd as ssd
-    return ssd
-
-
 def _io(x, name: str) -> int:
     if x.device.type != "cuda":
         raise ValueError(f"{name} runs on the GPU only (x is on {x.device})")
@@ -68,15 +65,21 @@ def _io(x, name: str) -> int:
     raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
 
 
-def _tokens(t, name, shape, dtype, device) -> int:
-    """Checks an activation and returns its token stride in elements: the last
-    dimension contiguous, all others collapsible to one (size-1 ones aside)."""
+def _refuse(t, name, shape, dtype, device):
+    """Says which of an argument's properties is wrong."""
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _tokens(t, name, shape, dtype, device) -> int:
+    """Checks an activation and returns its token stride in elements: the last
+    dimension contiguous, all others collapsible to one (size-1 ones aside)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(t, name, shape, dtype, device)
     if t.is_contiguous():
         return 0
     st, stride, span = t.stride(), None, 0
@@ -100,51 +103,54 @@ def _tokens(t, name, shape, dtype, device) -> int:
 
 def _dense(t, name, shape, dtype, device):
     if t is None:
-        return None
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+        return
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+# The current stream's handle of a device, without the Stream object around it
+# (2 us of a 10 us call) where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _On:
     """The device made current and, with a stream handle given, that stream
-    too: what is allocated inside belongs to the stream the kernels run on."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        elif stream == 0:
-            with torch.cuda.stream(torch.cuda.default_stream(device)):
-                yield 0
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-                yield stream
-
-
-class _Here:
-    """_on without its cost for the usual call: x's device is current already
-    and no stream is given."""
+    too: what is allocated inside belongs to the stream the kernels run on.
+    Does nothing for the usual call, x's device current and no stream given."""
+    __slots__ = ("index", "stack", "stream")
 
     def __init__(self, device, stream):
-        plain = stream is None and device.index == torch.cuda.current_device()
-        self.other = None if plain else _on(device, stream)
-        self.device = device
+        self.index, self.stream = device.index, stream
+        self.stack = None if stream is None and device.index == torch.cuda.current_device() else contextlib.ExitStack()
 
     def __enter__(self):
-        return torch.cuda.current_stream(self.device).cuda_stream if self.other is None else self.other.__enter__()
+        if self.stack is not None:
+            self.stack.enter_context(torch.cuda.device(self.index))
+            if self.stream is not None:
+                self.stack.enter_context(torch.cuda.stream(
+                    torch.cuda.ExternalStream(self.stream, device=self.index) if self.stream
+                    else torch.cuda.default_stream(self.index)))
+                return self.stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        return None if self.other is None else self.other.__exit__(*exc)
+        if self.stack is not None:
+            self.stack.close()
+
+
+def _like(given, name, x):
+    """An output of x's shape and type."""
+    if given is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    _dense(given, name, x.shape, x.dtype, x.device)
+    return given
 
 
 def _output(given, name, shape, dtype, device):
@@ -213,12 +219,11 @@ def ssd_glr_fwd(x, g, A, bias=None, z=None, seq_idx=None, init_states=None, norm
     fp32 state [b, D] after the last token (None without
     ``return_final_states``).  g, z as x; A (<= 0), bias [D], init_states
     [b, D]: fp32."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _glr_common("ssd_glr_fwd", x, g, A, bias, z, seq_idx, init_states, normalize)
     dev, b, D = x.device, shape.batch, shape.channels
-    with _Here(dev, stream) as st:
-        y = _output(y, "y", x.shape, x.dtype, dev)
+    with _On(dev, stream) as st:
+        y = _like(y, "y", x)
         if return_final_states or final_states is not None:
             final_states = _output(final_states, "final_states", (b, D), torch.float32, dev)
         need = int(lib.ssd_glr_fwd_workspace_bytes(ctypes.byref(shape), io))
@@ -237,14 +242,13 @@ def ssd_glr_bwd(x, g, A, bias, dy, z=None, seq_idx=None, init_states=None, dfina
     dx, dg, dz (x's dtype), dA, dbias [D] and dinit [b, D] (fp32); dz, dbias and
     dinit are None without z, bias and init_states.  dy as x; dfinal [b, D]
     fp32 or None.  ``out``: the outputs to write, every one that is returned."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _glr_common("ssd_glr_bwd", x, g, A, bias, z, seq_idx, init_states, normalize)
     dev, b, D, f32 = x.device, shape.batch, shape.channels, torch.float32
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
     _dense(dfinal, "dfinal", (b, D), f32, dev)
     act = (x.shape, x.dtype)
-    with _Here(dev, stream) as st:
+    with _On(dev, stream) as st:
         out = _outputs(out, {"dx": act, "dg": act, "dz": None if z is None else act, "dA": ((D,), f32),
                              "dbias": None if bias is None else ((D,), f32),
                              "dinit": None if init_states is None else ((b, D), f32)}, dev)
@@ -261,7 +265,6 @@ def ssd_glr_bwd(x, g, A, bias, dy, z=None, seq_idx=None, init_states=None, dfina
 def ssd_glr_step(x, g, A, state, bias=None, z=None, normalize: bool = True, y=None, stream=None) -> torch.Tensor:
     """One token of ssd_glr_fwd: x, g, z [b, D]; state [b, D] fp32 updated in
     place.  Returns y [b, D]."""
-    ssd = _binding()
     lib = ssd.load_library()
     io = _io(x, "ssd_glr_step")
     if x.dim() != 2:
@@ -273,8 +276,8 @@ def ssd_glr_step(x, g, A, state, bias=None, z=None, normalize: bool = True, y=No
     _dense(A, "A", (D,), f32, dev)
     _dense(bias, "bias", (D,), f32, dev)
     _dense(state, "state", (b, D), f32, dev)
-    with _Here(dev, stream) as st:
-        y = _output(y, "y", x.shape, dt, dev)
+    with _On(dev, stream) as st:
+        y = _like(y, "y", x)
         status = lib.ssd_glr_step(ctypes.byref(shape), io, x.data_ptr(), g.data_ptr(), A.data_ptr(), _ptr(bias), _ptr(z),
                                   state.data_ptr(), y.data_ptr(), st)
     ssd._check(status)
@@ -308,12 +311,11 @@ def ssd_conv_fwd(x, weight, bias=None, seq_idx=None, init_states=None, silu: boo
     one before it.  init_states [b, W-1, D] (x's dtype) are the inputs before
     the row.  Returns (y, final_states): the window [b, W-1, D] the next token
     sees (None without ``return_final_states``)."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _conv_common("ssd_conv_fwd", x, weight, bias, seq_idx, init_states, silu)
     dev = x.device
-    with _Here(dev, stream) as st:
-        y = _output(y, "y", x.shape, x.dtype, dev)
+    with _On(dev, stream) as st:
+        y = _like(y, "y", x)
         if return_final_states or final_states is not None:
             final_states = _output(final_states, "final_states", (shape.batch, shape.width - 1, shape.channels), x.dtype,
                                    dev)
@@ -329,14 +331,13 @@ def ssd_conv_bwd(x, weight, bias, dy, seq_idx=None, init_states=None, dfinal=Non
     of dx (x's dtype), dweight [D, W], dbias [D] (None without bias) and dinit
     [b, W-1, D] (None without init_states), fp32.  dy as x; dfinal [b, W-1, D]
     fp32 or None.  ``out``: the outputs to write, every one that is returned."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _conv_common("ssd_conv_bwd", x, weight, bias, seq_idx, init_states, silu)
     dev, f32 = x.device, torch.float32
     b, D, W = shape.batch, shape.channels, shape.width
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
     _dense(dfinal, "dfinal", (b, W - 1, D), f32, dev)
-    with _Here(dev, stream) as st:
+    with _On(dev, stream) as st:
         out = _outputs(out, {"dx": (x.shape, x.dtype), "dweight": ((D, W), f32),
                              "dbias": None if bias is None else ((D,), f32),
                              "dinit": None if init_states is None else ((b, W - 1, D), f32)}, dev)
@@ -352,7 +353,6 @@ def ssd_conv_bwd(x, weight, bias, dy, seq_idx=None, init_states=None, dfinal=Non
 def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream=None) -> torch.Tensor:
     """One token of ssd_conv_fwd: x [b, D]; state [b, W-1, D] (x's dtype), the
     last W-1 inputs, shifted in place.  Returns y [b, D]."""
-    ssd = _binding()
     lib = ssd.load_library()
     io = _io(x, "ssd_conv_step")
     if x.dim() != 2 or weight.dim() != 2:
@@ -364,8 +364,8 @@ def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream
     _dense(weight, "weight", (D, W), f32, dev)
     _dense(bias, "bias", (D,), f32, dev)
     _dense(state, "state", (b, W - 1, D), dt, dev)
-    with _Here(dev, stream) as st:
-        y = _output(y, "y", x.shape, dt, dev)
+    with _On(dev, stream) as st:
+        y = _like(y, "y", x)
         status = lib.ssd_conv_step(ctypes.byref(shape), io, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                                    state.data_ptr(), y.data_ptr(), st)
     ssd._check(status)
@@ -403,13 +403,12 @@ def ssd_norm_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5, ngrou
     groups, times weight [D] (fp32, None: 1): of x, of x + residual (rounded to
     x's dtype, the residual stream), or of x silu(z).  Returns (y, the residual
     stream or None).  ``residual_out`` may be ``residual`` itself."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _norm_fwd("ssd_norm_fwd", x, weight, residual, z, eps, ngroups, residual_out)
-    with _Here(x.device, stream) as st:
-        y = _output(y, "y", x.shape, x.dtype, x.device)
+    with _On(x.device, stream) as st:
+        y = _like(y, "y", x)
         if residual is not None:
-            residual_out = _output(residual_out, "residual_out", x.shape, x.dtype, x.device)
+            residual_out = _like(residual_out, "residual_out", x)
         status = lib.ssd_norm_fwd(ctypes.byref(shape), io, x.data_ptr(), _ptr(weight), _ptr(residual), _ptr(z),
                                   y.data_ptr(), _ptr(residual_out), st)
     ssd._check(status)
@@ -423,17 +422,16 @@ def ssd_norm_quant_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5,
     or None) with y = q * scale, q [..., D] float8_e4m3fn and one fp32 scale =
     max|y| / 448 for each ``block`` = 128 columns of a norm group, or for each
     norm group with ``block`` = 0: scales [..., ngroups * blocks]."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _norm_fwd("ssd_norm_quant_fwd", x, weight, residual, z, eps, ngroups, residual_out)
     shape.quant_block = block
     per = shape.columns // ngroups if ngroups > 0 else 0
     blocks = -(-per // block) if block > 0 else 1
-    with _Here(x.device, stream) as st:
+    with _On(x.device, stream) as st:
         q = _output(q, "q", x.shape, torch.float8_e4m3fn, x.device)
         scales = _output(scales, "scales", (*x.shape[:-1], max(ngroups, 0) * blocks), torch.float32, x.device)
         if residual is not None:
-            residual_out = _output(residual_out, "residual_out", x.shape, x.dtype, x.device)
+            residual_out = _like(residual_out, "residual_out", x)
         status = lib.ssd_norm_quant_fwd(ctypes.byref(shape), io, x.data_ptr(), _ptr(weight), _ptr(residual), _ptr(z),
                                         q.data_ptr(), scales.data_ptr(), _ptr(residual_out), st)
     ssd._check(status)
@@ -448,7 +446,6 @@ def ssd_norm_bwd(x, weight, dy, z=None, dresidual=None, eps: float = 1e-5, ngrou
     dresidual, the stream's gradient from its other uses, is added to dx, which
     is the gradient of x and of the residual alike.  ``out``: the outputs to
     write, every one that is returned."""
-    ssd = _binding()
     lib = ssd.load_library()
     io, shape = _norm_common("ssd_norm_bwd", x, weight, z, eps, ngroups)
     dev = x.device
@@ -456,7 +453,7 @@ def ssd_norm_bwd(x, weight, dy, z=None, dresidual=None, eps: float = 1e-5, ngrou
     if dresidual is not None:
         shape.dresidual_stride = _tokens(dresidual, "dresidual", x.shape, x.dtype, dev)
     act = (x.shape, x.dtype)
-    with _Here(dev, stream) as st:
+    with _On(dev, stream) as st:
         out = _outputs(out, {"dx": act, "dz": None if z is None else act,
                              "dweight": None if weight is None else ((x.shape[-1],), torch.float32)}, dev)
         need = int(lib.ssd_norm_bwd_workspace_bytes(ctypes.byref(shape), io)) if weight is not None else 0
