@@ -5,24 +5,21 @@
 // with x zero across a document start.  Tap j of token t is live when no
 // document starts in (t - j, t].  Memory-bound: x in, y out; the W multiplies
 // and the sigmoid are about 25 vector instructions an element.
+#include <type_traits>
+
 #include "ssd_layer.hpp"
 
 namespace ssd {
 
 constexpr int kConvTokens = 16;   // tokens a thread holds at a time
 
-// Document starts around token t0: bit i for token t0 - (W-1) + i, i < N.
+// Document starts around token t0: bit i for token t0 - (W-1) + i, i < N <= 32,
+// of the row's L; one lane looks at each.  Called by whole waves.
 template <int W, int N>
 __device__ inline uint32_t conv_cuts(const int32_t *seq, int t0, int L) {
-    uint32_t bits = 0;
-    int p = seq[min(max(t0 - W, 0), L - 1)];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int q = seq[min(max(t0 - (W - 1) + i, 0), L - 1)];
-        bits |= (q != p ? 1u : 0u) << i;
-        p = q;
-    }
-    return bits;
+    const int t = t0 - (W - 1) + (int)(threadIdx.x % 64);
+    const bool cut = seq[min(max(t, 0), L - 1)] != seq[min(max(t - 1, 0), L - 1)];
+    return (uint32_t)__ballot(cut) & (uint32_t)((1ull << N) - 1);
 }
 
 // Whether tap j reaches back from the token with bit `at` (compile-time j, at).
@@ -58,55 +55,92 @@ __device__ inline void conv_weights(const ConvArgs &a, int c, float (&w)[W][V], 
     }
 }
 
-// One thread: V channels x 16 tokens, the threads of a workgroup side by side
-// along the channels (no idle lanes at the end of a token's row), consecutive
-// workgroups on one XCD so that the W - 1 tokens before a chunk come from L2.
-template <typename IO, int V, int W, bool PACKED>
+// A wave's unit of work: 64 V channels (the last strip of a token may be short)
+// of T tokens of one row.
+struct ConvUnit {
+    int strip, chunk;
+    int64_t b;
+};
+
+__device__ inline ConvUnit conv_unit(uint32_t u, int nstrip, int nchunk) {
+    ConvUnit r;
+    r.strip = __builtin_amdgcn_readfirstlane(u % nstrip);
+    const uint32_t q = u / nstrip;
+    r.chunk = __builtin_amdgcn_readfirstlane(q % nchunk);
+    r.b = __builtin_amdgcn_readfirstlane(q / nchunk);
+    return r;
+}
+
+// Consecutive workgroups on one XCD, so that the W - 1 tokens before a chunk
+// come from L2; the rows' offsets in scalar registers.  Two channels a lane:
+// 79 us for 8 x 2048 x 5376 in bf16 (4.5 TB/s); four 86 us, eight 98 us, whose
+// registers leave half and a third of the waves, and 24 tokens instead of 16
+// 78 us.
+template <typename IO, int V, int W, bool PACKED, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     constexpr int T = kConvTokens;
-    const int D = a.channels, L = a.seqlen, per = D / V, nch = (L + T - 1) / T;
-    const int64_t first = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * 256;
-    const uint32_t r = (uint32_t)(first % per) + threadIdx.x;
-    const int64_t q = first / per + r / (uint32_t)per;   // (row, chunk)
-    if (q >= (int64_t)a.batch * nch) return;
-    const int c = (int)(r % (uint32_t)per) * V;
-    const int64_t b = q / nch;
-    const int t0 = (int)(q % nch) * T;
-    Pack<IO, V> xr[T + W - 1];
-    const char *xb = (const char *)a.x + (b * L + t0) * a.xs + c * (int64_t)sizeof(IO);
-#pragma unroll
-    for (int i = 0; i < T; ++i) xr[W - 1 + i] = load_pack<IO, V>(xb + min(i, L - 1 - t0) * a.xs);
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) xr[i] = conv_x<IO, V, W>(a, b, t0 - (W - 1) + i, c);
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
+    const int D = a.channels, L = a.seqlen, nchunk = (L + T - 1) / T, nstrip = (D + 64 * V - 1) / (64 * V);
+    const uint32_t unit = (uint32_t)xcd_contiguous(blockIdx.x, gridDim.x) * 4 + threadIdx.x / 64;
+    if (unit >= (uint32_t)((int64_t)a.batch * nchunk * nstrip)) return;
+    const ConvUnit u = conv_unit(unit, nstrip, nchunk);
+    const int c0 = (u.strip * 64 + threadIdx.x % 64) * V;
+    const int c = min(c0, D - V);   // lanes past the last channel repeat it, and store nothing
+    const int t0 = u.chunk * T;
+    const int32_t *seq = PACKED ? a.seq_idx + u.b * L : nullptr;
+    const uint32_t cb = (uint32_t)c * (uint32_t)sizeof(IO);
+    const uint32_t cuts = PACKED ? conv_cuts<W, T + W - 1>(seq, t0, L) : 0u;
+    const __amdgpu_buffer_rsrc_t yb = buffer_of((IO *)a.y + (u.b * L + t0) * D);
     float w[W][V], bias[V];
     conv_weights<V, W>(a, c, w, bias);
-    const uint32_t cuts = PACKED ? conv_cuts<W, T + W - 1>(a.seq_idx + b * L, t0, L) : 0u;
-    IO *yb = (IO *)a.y + (b * L + t0) * D + c;
+    // INNER: a whole chunk inside a row, no document start in it, whole strip
+    auto chunk = [&](auto inner) {
+        constexpr bool INNER = decltype(inner)::value;
+        R xr[T + W - 1];
+        if (INNER) {
+            const __amdgpu_buffer_rsrc_t xb = buffer_of((const char *)a.x + (u.b * L + t0 - (W - 1)) * a.xs);
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-        float o[V];
+            for (int i = 0; i < T + W - 1; ++i) xr[i] = buffer_load<R>(xb, cb, (uint32_t)(i * a.xs));
+        } else {
+            const __amdgpu_buffer_rsrc_t xb = buffer_of((const char *)a.x + (u.b * L + t0) * a.xs);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float p = bias[v];
+            for (int i = 0; i < T; ++i) xr[W - 1 + i] = buffer_load<R>(xb, cb, (uint32_t)(min(i, L - 1 - t0) * a.xs));
 #pragma unroll
-            for (int j = W - 1; j >= 0; --j) {
-                const float x = (float)xr[W - 1 + i - j].v[v];
-                p = fmaf(w[W - 1 - j][v], !PACKED || conv_live(cuts, W - 1 + i, j) ? x : 0.f, p);
-            }
-            o[v] = a.silu ? p * sigmoid_f32(p) : p;
+            for (int i = 0; i < W - 1; ++i)
+                xr[i] = __builtin_bit_cast(R, conv_x<IO, V, W>(a, u.b, t0 - (W - 1) + i, c));
         }
-        if (t0 + i < L) store_pack<IO, V>(yb + (int64_t)i * D, o);
-    }
-    if (a.final_states && t0 + T >= L) {
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float p = bias[v];
+#pragma unroll
+                for (int j = W - 1; j >= 0; --j) {
+                    const float x = RW::at(xr[W - 1 + i - j], v);
+                    p = fmaf(w[W - 1 - j][v], INNER || !PACKED || conv_live(cuts, W - 1 + i, j) ? x : 0.f, p);
+                }
+                o[v] = SILU ? p * sigmoid_f32(p) : p;
+            }
+            if (INNER || (t0 + i < L && c0 < D))
+                buffer_store<IO, V>(yb, cb, (uint32_t)i * (uint32_t)D * (uint32_t)sizeof(IO), o);
+        }
+    };
+    if (t0 > 0 && t0 + T <= L && !cuts && (u.strip + 1) * 64 * V <= D)
+        chunk(std::true_type{});
+    else
+        chunk(std::false_type{});
+    if (a.final_states && t0 + T >= L && c0 < D) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int t = L - (W - 1) + j;
-            Pack<IO, V> f = conv_x<IO, V, W>(a, b, t, c);
-            if (PACKED && conv_cut_after(a.seq_idx + b * L, t, L)) {
+            Pack<IO, V> f = conv_x<IO, V, W>(a, u.b, t, c);
+            if (PACKED && conv_cut_after(seq, t, L)) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) f.v[v] = (IO)0.f;
             }
-            *(Pack<IO, V> *)((IO *)a.final_states + (b * (W - 1) + j) * D + c) = f;
+            *(Pack<IO, V> *)((IO *)a.final_states + (u.b * (W - 1) + j) * D + c) = f;
         }
     }
 }
@@ -116,23 +150,30 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
 // formed for the chunk's tokens and the W - 1 after them (p recomputed);
 // dx_t = sum_j w[W-1-j] ds_{t+j} over the live taps, and the weight's sums stay in
 // registers over the run, joined over the four waves in order and written as
-// one part per workgroup.
-template <typename IO, int V, int W, bool PACKED>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int run) {
+// one part per workgroup.  The chunks inside a row without a document start
+// are taken first, in a loop without a mask or a bound; the others after
+// them, in a loop of their own, so that neither's registers add to the
+// other's.
+template <typename IO, int V, int W, bool PACKED, bool SILU>
+__global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvArgs a, int run) {
     constexpr int T = kConvTokens, N = T + W - 1;
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     __shared__ float red[W + 1][4][64 * V];
     const int D = a.channels, L = a.seqlen;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int nstrip = (D + 64 * V - 1) / (64 * V), nrun = (L + run - 1) / run;
-    const int u = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int strip = u % nstrip, part = u / nstrip;
+    const uint32_t u = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int strip = __builtin_amdgcn_readfirstlane(u % nstrip), part = __builtin_amdgcn_readfirstlane(u / nstrip);
     const int64_t b = part / nrun;
     const int c0 = (strip * 64 + lane) * V;
     const bool cok = c0 < D;
     const int c = cok ? c0 : D - V;
-    const int begin = (part % nrun) * run + wave * (run / 4);
+    const uint32_t cb = (uint32_t)c * (uint32_t)sizeof(IO);
+    const int begin = __builtin_amdgcn_readfirstlane((part % nrun) * run + wave * (run / 4));
     const int end = min(L, begin + run / 4);
     const int32_t *seq = PACKED ? a.seq_idx + b * L : nullptr;
+    const bool whole = (strip + 1) * 64 * V <= D;
     float w[W][V], bias[V], dw[W][V], db[V];
     conv_weights<V, W>(a, c, w, bias);
 #pragma unroll
@@ -141,34 +182,46 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int run) {
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
     }
-    for (int t0 = begin; t0 < end; t0 += T) {
-        Pack<IO, V> xr[N + W - 1], dr[N];
-        const char *xb = (const char *)a.x + (b * L + t0) * a.xs + c * (int64_t)sizeof(IO);
-        const char *db_ = (const char *)a.dy + (b * L + t0) * a.dys + c * (int64_t)sizeof(IO);
+    auto cuts_at = [&](int t0) { return PACKED ? conv_cuts<W, N + W - 1>(seq, t0, L) : 0u; };
+    auto is_inner = [&](int t0, uint32_t cuts) { return t0 > 0 && t0 + N <= L && !cuts && whole; };
+    auto chunk = [&](int t0, uint32_t cuts, auto inner) {
+        constexpr bool INNER = decltype(inner)::value;
+        constexpr bool MASKED = PACKED && !INNER;
+        R xr[N + W - 1], dr[N];
+        const __amdgpu_buffer_rsrc_t gb = buffer_of((const char *)a.dy + (b * L + t0) * a.dys);
+        if (INNER) {
+            const __amdgpu_buffer_rsrc_t xb = buffer_of((const char *)a.x + (b * L + t0 - (W - 1)) * a.xs);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = min(i, L - 1 - t0);
-            xr[W - 1 + i] = load_pack<IO, V>(xb + k * a.xs);
-            dr[i] = load_pack<IO, V>(db_ + k * a.dys);
+            for (int i = 0; i < N + W - 1; ++i) xr[i] = buffer_load<R>(xb, cb, (uint32_t)(i * a.xs));
+#pragma unroll
+            for (int i = 0; i < N; ++i) dr[i] = buffer_load<R>(gb, cb, (uint32_t)(i * a.dys));
+        } else {
+            const __amdgpu_buffer_rsrc_t xb = buffer_of((const char *)a.x + (b * L + t0) * a.xs);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = min(i, L - 1 - t0);
+                xr[W - 1 + i] = buffer_load<R>(xb, cb, (uint32_t)(k * a.xs));
+                dr[i] = buffer_load<R>(gb, cb, (uint32_t)(k * a.dys));
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) xr[i] = __builtin_bit_cast(R, conv_x<IO, V, W>(a, b, t0 - (W - 1) + i, c));
         }
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i) xr[i] = conv_x<IO, V, W>(a, b, t0 - (W - 1) + i, c);
-        const uint32_t cuts = PACKED ? conv_cuts<W, N + W - 1>(seq, t0, L) : 0u;
+        const __amdgpu_buffer_rsrc_t ob = buffer_of((IO *)a.dx + (b * L + t0) * D);
         float ds[N][V];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const bool in = t0 + i < L;
+            const bool in = INNER || t0 + i < L;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float xl[W], p = bias[v];
 #pragma unroll
                 for (int j = W - 1; j >= 0; --j) {
-                    const float x = (float)xr[W - 1 + i - j].v[v];
-                    xl[j] = !PACKED || conv_live(cuts, W - 1 + i, j) ? x : 0.f;
+                    const float x = RW::at(xr[W - 1 + i - j], v);
+                    xl[j] = !MASKED || conv_live(cuts, W - 1 + i, j) ? x : 0.f;
                     p = fmaf(w[W - 1 - j][v], xl[j], p);
                 }
-                float d = (float)dr[i].v[v];
-                if (a.silu) {
+                float d = RW::at(dr[i], v);
+                if (SILU) {
                     const float s = sigmoid_f32(p);
                     d *= s * fmaf(p, 1.f - s, 1.f);
                 }
@@ -188,23 +241,22 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int run) {
                     float s = 0.f;
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        const float d = !PACKED || conv_live(cuts, W - 1 + o + j, j) ? ds[o + j][v] : 0.f;
+                        const float d = !MASKED || conv_live(cuts, W - 1 + o + j, j) ? ds[o + j][v] : 0.f;
                         s = fmaf(w[W - 1 - j][v], d, s);
                     }
                     dx[v] = s;
                 }
                 const int t = t0 + o;
-                if (t < L) {
-                    if (a.dfinal && t >= L - (W - 1) && !(PACKED && conv_cut_after(seq, t, L))) {
+                // (an inner chunk ends before the tokens of the final window)
+                if (!INNER && a.dfinal && t < L && t >= L - (W - 1) && !(PACKED && conv_cut_after(seq, t, L))) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            dx[v] += a.dfinal[(b * (W - 1) + t - (L - (W - 1))) * D + c + v];
-                    }
-                    if (cok) store_pack<IO, V>((IO *)a.dx + (b * L + t) * D + c, dx);
+                    for (int v = 0; v < V; ++v) dx[v] += a.dfinal[(b * (W - 1) + t - (L - (W - 1))) * D + c + v];
                 }
+                if (INNER || (t < L && cok))
+                    buffer_store<IO, V>(ob, cb, (uint32_t)o * (uint32_t)D * (uint32_t)sizeof(IO), dx);
             }
         }
-        if (a.dinit && t0 == 0 && cok) {
+        if (!INNER && a.dinit && t0 == 0 && cok) {
             // the window before the row: tokens -(W-1) .. -1
 #pragma unroll
             for (int q = 0; q < W - 1; ++q) {
@@ -216,7 +268,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int run) {
 #pragma unroll
                     for (int j = 1; j < W; ++j)
                         if (t + j >= 0) {
-                            const float d = !PACKED || conv_live(cuts, W - 1 + t + j, j) ? ds[t + j >= 0 ? t + j : 0][v] : 0.f;
+                            const float d = !MASKED || conv_live(cuts, W - 1 + t + j, j) ? ds[t + j >= 0 ? t + j : 0][v] : 0.f;
                             s = fmaf(w[W - 1 - j][v], d, s);
                         }
                     if (out) s += a.dfinal[(b * (W - 1) + t - (L - (W - 1))) * D + c + v];
@@ -224,6 +276,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int run) {
                 }
             }
         }
+    };
+    for (int t0 = begin; t0 < end; t0 += T) {
+        const uint32_t cuts = cuts_at(t0);
+        if (is_inner(t0, cuts)) chunk(t0, cuts, std::true_type{});
+    }
+    for (int t0 = begin; t0 < end; t0 += T) {
+        const uint32_t cuts = cuts_at(t0);
+        if (!is_inner(t0, cuts)) chunk(t0, cuts, std::false_type{});
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -267,22 +327,34 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
     store_pack<IO, V>((IO *)a.y + b * D + c, o);
 }
 
-int conv_strip(bool bf16_io, bool wide) { return 64 * (wide ? 4 : 1); }
+// Channels of a wave's strip.
+int conv_strip(bool pair) { return 64 * (pair ? 2 : 1); }
+
+template <typename IO, int V, int W, bool PACKED>
+static void conv_fwd_launch_docs(const ConvArgs &a, unsigned grid, hipStream_t stream) {
+    if (a.silu)
+        hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, PACKED, true>), dim3(grid), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, PACKED, false>), dim3(grid), dim3(256), 0, stream, a);
+}
 
 template <typename IO, int V, int W>
 static void conv_fwd_launch(const ConvArgs &a, unsigned grid, hipStream_t stream) {
-    if (a.seq_idx)
-        hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, true>), dim3(grid), dim3(256), 0, stream, a);
+    a.seq_idx ? conv_fwd_launch_docs<IO, V, W, true>(a, grid, stream) : conv_fwd_launch_docs<IO, V, W, false>(a, grid, stream);
+}
+
+template <typename IO, int V, int W, bool PACKED>
+static void conv_bwd_launch_docs(const ConvArgs &a, int run, unsigned grid, hipStream_t stream) {
+    if (a.silu)
+        hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, PACKED, true>), dim3(grid), dim3(256), 0, stream, a, run);
     else
-        hipLaunchKernelGGL((conv_fwd_kernel<IO, V, W, false>), dim3(grid), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, PACKED, false>), dim3(grid), dim3(256), 0, stream, a, run);
 }
 
 template <typename IO, int V, int W>
 static void conv_bwd_launch(const ConvArgs &a, int run, unsigned grid, hipStream_t stream) {
-    if (a.seq_idx)
-        hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, true>), dim3(grid), dim3(256), 0, stream, a, run);
-    else
-        hipLaunchKernelGGL((conv_bwd_kernel<IO, V, W, false>), dim3(grid), dim3(256), 0, stream, a, run);
+    a.seq_idx ? conv_bwd_launch_docs<IO, V, W, true>(a, run, grid, stream)
+              : conv_bwd_launch_docs<IO, V, W, false>(a, run, grid, stream);
 }
 
 template <typename IO, int V, int W>
@@ -297,40 +369,32 @@ static void conv_step_launch(const ConvArgs &a, unsigned grid, hipStream_t strea
     default: launch<IO, V, 4>(a, __VA_ARGS__, stream);       \
     }
 
-// Elements per access of the forward pass: 16 bytes when all is aligned for it.
-int conv_fwd_vec(bool bf16_io, bool wide) { return wide ? (bf16_io ? 8 : 4) : 1; }
-
-void launch_conv_fwd(bool bf16_io, bool wide, const ConvArgs &a, hipStream_t stream) {
-    const int64_t chunks = (a.seqlen + kConvTokens - 1) / kConvTokens;
-    const int64_t threads = a.batch * chunks * (a.channels / conv_fwd_vec(bf16_io, wide));
-    const unsigned grid = (unsigned)((threads + 255) / 256);
-    if (bf16_io) {
-        if (wide) { SSD_CONV_BY_WIDTH(conv_fwd_launch, bf16, 8, grid) } else { SSD_CONV_BY_WIDTH(conv_fwd_launch, bf16, 1, grid) }
-    } else {
-        if (wide) { SSD_CONV_BY_WIDTH(conv_fwd_launch, float, 4, grid) } else { SSD_CONV_BY_WIDTH(conv_fwd_launch, float, 1, grid) }
+#define SSD_CONV_BY_TYPE(launch, ...)                                                                              \
+    if (bf16_io) {                                                                                                 \
+        if (pair) { SSD_CONV_BY_WIDTH(launch, bf16, 2, __VA_ARGS__) } else { SSD_CONV_BY_WIDTH(launch, bf16, 1, __VA_ARGS__) }   \
+    } else {                                                                                                       \
+        if (pair) { SSD_CONV_BY_WIDTH(launch, float, 2, __VA_ARGS__) } else { SSD_CONV_BY_WIDTH(launch, float, 1, __VA_ARGS__) } \
     }
+
+void launch_conv_fwd(bool bf16_io, bool pair, const ConvArgs &a, hipStream_t stream) {
+    const int strip = conv_strip(pair);
+    const int64_t units = a.batch * (int64_t)((a.seqlen + kConvTokens - 1) / kConvTokens) * ((a.channels + strip - 1) / strip);
+    const unsigned grid = (unsigned)((units + 3) / 4);
+    SSD_CONV_BY_TYPE(conv_fwd_launch, grid)
 }
 
-void launch_conv_bwd(bool bf16_io, bool wide, const ConvArgs &a, int run, float *dweight, float *dbias,
+void launch_conv_bwd(bool bf16_io, bool pair, const ConvArgs &a, int run, float *dweight, float *dbias,
                      hipStream_t stream) {
-    const int strip = conv_strip(bf16_io, wide);
+    const int strip = conv_strip(pair);
     const int64_t parts = (int64_t)a.batch * ((a.seqlen + run - 1) / run);
     const unsigned grid = (unsigned)(parts * ((a.channels + strip - 1) / strip));
-    if (bf16_io) {
-        if (wide) { SSD_CONV_BY_WIDTH(conv_bwd_launch, bf16, 4, run, grid) } else { SSD_CONV_BY_WIDTH(conv_bwd_launch, bf16, 1, run, grid) }
-    } else {
-        if (wide) { SSD_CONV_BY_WIDTH(conv_bwd_launch, float, 4, run, grid) } else { SSD_CONV_BY_WIDTH(conv_bwd_launch, float, 1, run, grid) }
-    }
+    SSD_CONV_BY_TYPE(conv_bwd_launch, run, grid)
     launch_part_sum(a.part, parts, a.channels, a.width, dweight, dbias, stream);
 }
 
 void launch_conv_step(bool bf16_io, bool pair, const ConvArgs &a, hipStream_t stream) {
     const unsigned grid = (unsigned)(((int64_t)a.batch * (a.channels / (pair ? 2 : 1)) + 255) / 256);
-    if (bf16_io) {
-        if (pair) { SSD_CONV_BY_WIDTH(conv_step_launch, bf16, 2, grid) } else { SSD_CONV_BY_WIDTH(conv_step_launch, bf16, 1, grid) }
-    } else {
-        if (pair) { SSD_CONV_BY_WIDTH(conv_step_launch, float, 2, grid) } else { SSD_CONV_BY_WIDTH(conv_step_launch, float, 1, grid) }
-    }
+    SSD_CONV_BY_TYPE(conv_step_launch, grid)
 }
 
 }  // namespace ssd

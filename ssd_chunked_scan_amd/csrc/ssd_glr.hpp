@@ -132,6 +132,17 @@ __device__ inline uint32_t glr_resets(const int32_t *seq, int t, int L) {
     return bits;
 }
 
+// The same for a lane whose wave's segments follow each other from token t of
+// the row on, one lane looking at each token.  Called by whole waves.
+template <typename TL>
+__device__ inline uint32_t glr_wave_resets(const int32_t *seq, int t, int L) {
+    static_assert(TL::TL * TL::T <= 64, "a lane per token");
+    const int k = t + (int)(threadIdx.x % 64);
+    const bool cut = seq[min(k, L - 1)] != seq[min(max(k - 1, 0), L - 1)];
+    const uint64_t bits = __ballot(cut);
+    return (uint32_t)(bits >> (threadIdx.x % 64 / TL::CL * TL::T)) & ((1u << TL::T) - 1u);
+}
+
 // h after the maps of the segments before `seg` (wave `wave`'s are TL::TL in a
 // row): whole waves first, so that their maps are read together.
 template <bool PACKED, typename TL>
@@ -227,7 +238,7 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
     };
     auto round = [&](int t, int buf, auto full) {
         constexpr bool FULL = decltype(full)::value;
-        const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t + m, L) : 0u;
+        const uint32_t cut = PACKED ? glr_wave_resets<TL>(a.seq_idx + row, t + tid / 64 * (TL::TL * T), L) : 0u;
         float p[T][V], q[T][V];
 #pragma unroll
         for (int i = 0; i < T; ++i) {
@@ -423,7 +434,7 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel
         glr_load<FULL>(xr, xb, a.xs, m, cb, L - t);
         glr_load<FULL>(dr, db, a.dys, m, cb, L - t);
         if (GATE) glr_load<FULL>(zr, zb, a.zs, m, cb, L - t);
-        const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t + m, L) : 0u;
+        const uint32_t cut = PACKED ? glr_wave_resets<TL>(a.seq_idx + row, t + tid / 64 * (TL::TL * T), L) : 0u;
         float A[V], bias[V], hin[V], cin[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {

@@ -104,15 +104,20 @@ template <>
 struct Words<4> { typedef uint32_t type; };
 template <>
 struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+template <>
+struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
 
 template <typename IO, int V>
 struct Raw {
     typedef typename Words<sizeof(IO) * V>::type type;
+    static __device__ inline uint32_t word(type r, int i) {
+        if constexpr (sizeof(IO) * V <= 4) return r;
+        else return r[i];
+    }
     static __device__ inline float at(type r, int v) {
-        if constexpr (sizeof(IO) * V == 2) return __uint_as_float((uint32_t)r << 16);
-        else if constexpr (sizeof(IO) == 4 && V == 1) return __uint_as_float(r);
-        else if constexpr (sizeof(IO) == 4) return __uint_as_float(r[v]);
-        else return __uint_as_float(v ? r & 0xffff0000u : r << 16);
+        if constexpr (sizeof(IO) == 4) return __uint_as_float(word(r, v));
+        else if constexpr (V == 1) return __uint_as_float((uint32_t)r << 16);
+        else return __uint_as_float(v % 2 ? word(r, v / 2) & 0xffff0000u : word(r, v / 2) << 16);
     }
 };
 
@@ -128,7 +133,8 @@ template <typename R>
 __device__ inline R buffer_load(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t token) {
     if constexpr (sizeof(R) == 2) return __builtin_amdgcn_raw_buffer_load_b16(b, lane, token, 0);
     else if constexpr (sizeof(R) == 4) return __builtin_amdgcn_raw_buffer_load_b32(b, lane, token, 0);
-    else return __builtin_amdgcn_raw_buffer_load_b64(b, lane, token, 0);
+    else if constexpr (sizeof(R) == 8) return __builtin_amdgcn_raw_buffer_load_b64(b, lane, token, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b128(b, lane, token, 0);
 }
 
 template <typename IO, int V>
@@ -139,7 +145,8 @@ __device__ inline void buffer_store(__amdgpu_buffer_rsrc_t b, uint32_t lane, uin
     const R r = __builtin_bit_cast(R, __builtin_convertvector(__builtin_bit_cast(fv, f), iv));
     if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(r, b, lane, token, 0);
     else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(r, b, lane, token, 0);
-    else __builtin_amdgcn_raw_buffer_store_b64(r, b, lane, token, 0);
+    else if constexpr (sizeof(R) == 8) __builtin_amdgcn_raw_buffer_store_b64(r, b, lane, token, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(r, b, lane, token, 0);
 }
 
 // ------------------------------------------------------------------- maps

@@ -17,10 +17,9 @@ int compute_units(hipStream_t stream);
 void launch_glr_fwd(bool bf16_io, bool pair, const GlrArgs &a, hipStream_t stream);
 void launch_glr_bwd(bool bf16_io, bool pair, const GlrArgs &a, hipStream_t stream);
 void launch_glr_step(bool bf16_io, bool pair, const GlrStepArgs &a, hipStream_t stream);
-int conv_fwd_vec(bool bf16_io, bool wide);
-int conv_strip(bool bf16_io, bool wide);
-void launch_conv_fwd(bool bf16_io, bool wide, const ConvArgs &a, hipStream_t stream);
-void launch_conv_bwd(bool bf16_io, bool wide, const ConvArgs &a, int run, float *dweight, float *dbias,
+int conv_strip(bool pair);
+void launch_conv_fwd(bool bf16_io, bool pair, const ConvArgs &a, hipStream_t stream);
+void launch_conv_bwd(bool bf16_io, bool pair, const ConvArgs &a, int run, float *dweight, float *dbias,
                      hipStream_t stream);
 void launch_conv_step(bool bf16_io, bool pair, const ConvArgs &a, hipStream_t stream);
 void launch_norm_fwd(bool bf16_io, bool wide, const NormArgs &a, hipStream_t stream);
@@ -201,8 +200,9 @@ ssd_status_t check_conv(const ssd_conv_shape_t *s, ssd_dtype_t io) {
     SSD_TRY(check_stride("dy", s->dy_stride, s->channels));
     if (s->silu != 0 && s->silu != 1) return fail(SSD_ERR_UNSUPPORTED, "silu must be 0 or 1, got %lld", (long long)s->silu);
     SSD_TRY(check_reserved(s->reserved));
-    // single channels: 16 tokens x 256 channels (forward), 64 x 64 (backward)
-    const int64_t fwd = (s->batch * ((s->seqlen + 15) / 16) * s->channels + 255) / 256;
+    // single channels: a wave per 16 tokens x 64 channels (forward), a workgroup
+    // per 64 x 64 (backward)
+    const int64_t fwd = (s->batch * ((s->seqlen + 15) / 16) * ((s->channels + 63) / 64) + 3) / 4;
     const int64_t bwd = s->batch * ((s->seqlen + 63) / 64) * ((s->channels + 63) / 64);
     if (fwd > kMaxGrid || bwd > kMaxGrid) return fail(SSD_ERR_UNSUPPORTED, "problem too large");
     return SSD_OK;
@@ -450,11 +450,10 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     ssd::ConvArgs a = conv_args(shape, io, x, weight, bias, seq_idx, init_states);
     a.y = y;
     a.final_states = final_states;
-    const int n = wide_of(io);
     const int64_t dense = shape->channels * (int64_t)e;
-    const bool wide = Access(shape->channels % n == 0, n, io).in(x, a.xs).in(init_states, dense).in(y, dense)
+    const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(init_states, dense).in(y, dense)
                           .in(final_states, dense).ok;
-    ssd::launch_conv_fwd(io == SSD_BF16, wide, a, (hipStream_t)stream);
+    ssd::launch_conv_fwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_conv_fwd");
 }
 
@@ -493,10 +492,10 @@ ssd_status_t ssd_conv_bwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     a.dinit = dinit;
     a.part = (float *)workspace;
     const int64_t dense = shape->channels * (int64_t)e;
-    const bool wide = Access(shape->channels % 4 == 0, 4, io).in(x, a.xs).in(dy, a.dys).in(init_states, dense)
+    const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(dy, a.dys).in(init_states, dense)
                           .in(dx, dense).ok;
-    const int run = conv_run(shape, ssd::conv_strip(io == SSD_BF16, wide), (hipStream_t)stream);
-    ssd::launch_conv_bwd(io == SSD_BF16, wide, a, run, dweight, dbias, (hipStream_t)stream);
+    const int run = conv_run(shape, ssd::conv_strip(pair), (hipStream_t)stream);
+    ssd::launch_conv_bwd(io == SSD_BF16, pair, a, run, dweight, dbias, (hipStream_t)stream);
     return launched("ssd_conv_bwd");
 }
 
