@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
 // them, in a loop of their own, so that neither's registers add to the
 // other's.
 template <typename IO, int V, int W, bool PACKED, bool SILU>
-__global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvArgs a, int run) {
+__global__ __launch_bounds__(256, sizeof(IO) == 2 ? 4 : 1) void conv_bwd_kernel(ConvArgs a, int run) {
     constexpr int T = kConvTokens, N = T + W - 1;
     typedef Raw<IO, V> RW;
     typedef typename RW::type R;

@@ -43,9 +43,10 @@ typedef GlrTile<2, 32, 8, 8> GlrFwdPair;
 typedef GlrTile<1, 32, 16, 4> GlrFwdSingle;
 typedef GlrTile<2, 32, 4, 8> GlrBwdPair;
 typedef GlrTile<1, 32, 8, 4> GlrBwdSingle;
+typedef GlrTile<2, 32, 8, 4> GlrBlockPair;   // the backward blocks' maps: nothing stays
 constexpr int kGlrFwdRound = 128, kGlrBwdBlock = 64;   // tokens a forward round, a backward block
 static_assert(GlrFwdPair::RT == kGlrFwdRound && GlrFwdSingle::RT == kGlrFwdRound, "");
-static_assert(GlrBwdPair::RT == kGlrBwdBlock && GlrBwdSingle::RT == kGlrBwdBlock, "");
+static_assert(GlrBwdPair::RT == kGlrBwdBlock && GlrBwdSingle::RT == kGlrBwdBlock && GlrBlockPair::RT == kGlrBwdBlock, "");
 
 constexpr float kGlrReset = -0.f;
 __device__ inline bool glr_is_reset(float p) { return __float_as_int(p) < 0; }
@@ -408,12 +409,12 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
 //   dg = A dla sigmoid(g + bias)   dA = sum s dla   dbias = sum dg
 //   dz = dy h silu'(z)
 template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
-__global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel(GlrArgs a) {
+__global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACKED && GATE) ? 4 : 1) void glr_bwd_kernel(GlrArgs a) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
     typedef Raw<IO, V> RW;
     typedef typename RW::type R;
     __shared__ float2 seg_map[SEG][CT];
-    __shared__ float seg_e[SEG][CT];
+    __shared__ float seg_e[SEG][CT], seg_h[SEG][CT];
     const GlrUnit u = glr_unit<TL>(a, a.nblk);
     const int tid = threadIdx.x, cg = tid % TL::CL, seg = tid / TL::CL, m = seg * T;
     const int D = a.channels, L = a.seqlen;
@@ -422,7 +423,6 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel
     const int cc = cok ? c : D - V, cb = cc * (int)sizeof(IO);
     const int t = u.blk * TL::RT;
     const int64_t row = (int64_t)u.b * L;
-    const int64_t wsat = ((int64_t)u.b * a.nblk + u.blk) * D + cc;
     const int64_t ys = (int64_t)D * (int)sizeof(IO);
     const char *gb = (const char *)a.g + (row + t) * a.gs, *xb = (const char *)a.x + (row + t) * a.xs;
     const char *db = (const char *)a.dy + (row + t) * a.dys, *zb = (const char *)a.z + (row + t) * a.zs;
@@ -435,13 +435,11 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel
         glr_load<FULL>(dr, db, a.dys, m, cb, L - t);
         if (GATE) glr_load<FULL>(zr, zb, a.zs, m, cb, L - t);
         const uint32_t cut = PACKED ? glr_wave_resets<TL>(a.seq_idx + row, t + tid / 64 * (TL::TL * T), L) : 0u;
-        float A[V], bias[V], hin[V], cin[V];
+        float A[V], bias[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             A[v] = a.A[cc + v];
             bias[v] = a.bias ? a.bias[cc + v] : 0.f;
-            hin[v] = a.ws_h[wsat + v];
-            cin[v] = a.ws_e[wsat + v];
         }
         auto ok = [&](int i) { return FULL || t + m + i < L; };
         // decay, input factor, softplus (base 2) and its derivative, the
@@ -481,11 +479,36 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 ? 4 : 1) void glr_bwd_kernel
             seg_e[seg][cg * V + v] = es;
         }
         __syncthreads();
-        glr_enter<PACKED, TL>(hin, seg_map, cg * V, seg);
-        for (int s = SEG - 1; s > seg; --s)
+        // the segments are joined by a thread per channel and direction, which
+        // costs a barrier and spares each lane the maps on both its sides
+        if (tid < 2 * CT && u.ct * CT + tid % CT < D) {
+            const int ch = tid % CT;
+            const int64_t at = ((int64_t)u.b * a.nblk + u.blk) * D + u.ct * CT + ch;
+            if (tid < CT) {
+                float hv = a.ws_h[at];
+#pragma unroll 4
+                for (int s = 0; s < SEG; ++s) {
+                    const float2 f = seg_map[s][ch];
+                    seg_h[s][ch] = hv;
+                    hv = glr_apply<PACKED>(f.x, hv, f.y);
+                }
+            } else {
+                float ev = a.ws_e[at];
+#pragma unroll 4
+                for (int s = SEG - 1; s >= 0; --s) {
+                    const float p = seg_map[s][ch].x, own = seg_e[s][ch];
+                    seg_e[s][ch] = ev;
+                    ev = glr_apply<PACKED>(p, ev, own);
+                }
+            }
+        }
+        __syncthreads();
+        float hin[V], cin[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                cin[v] = glr_apply<PACKED>(seg_map[s][cg * V + v].x, cin[v], seg_e[s][cg * V + v]);
+        for (int v = 0; v < V; ++v) {
+            hin[v] = seg_h[seg][cg * V + v];
+            cin[v] = seg_e[seg][cg * V + v];
+        }
         float h[T][V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -584,10 +607,12 @@ void launch_glr_block_scan(const GlrArgs &a, hipStream_t stream);
 
 template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
 void launch_glr_bwd_gate(const GlrArgs &a, hipStream_t stream) {
-    const dim3 grid = glr_grid<TL>(a, a.nblk), block(TL::W * 64);
-    hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, true, GATE>), grid, block, 0, stream, a, a.nblk);
+    typedef typename std::conditional<TL::V == 2, GlrBlockPair, TL>::type BL;
+    hipLaunchKernelGGL((glr_block_kernel<IO, BL, NORM, PACKED, true, GATE>), glr_grid<BL>(a, a.nblk), dim3(BL::W * 64),
+                       0, stream, a, a.nblk);
     launch_glr_block_scan(a, stream);
-    hipLaunchKernelGGL((glr_bwd_kernel<IO, TL, NORM, PACKED, GATE>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((glr_bwd_kernel<IO, TL, NORM, PACKED, GATE>), glr_grid<TL>(a, a.nblk), dim3(TL::W * 64), 0,
+                       stream, a);
 }
 
 template <typename IO, typename TL, bool NORM, bool PACKED>
