@@ -44,6 +44,15 @@ typedef GlrTile<1, 32, 16, 4> GlrFwdSingle;
 typedef GlrTile<2, 32, 4, 8> GlrBwdPair;
 typedef GlrTile<1, 32, 8, 4> GlrBwdSingle;
 typedef GlrTile<2, 32, 8, 4> GlrBlockPair;   // the backward blocks' maps: nothing stays
+// Rows of at most 16 tokens, where the long tiles' waves would mostly be past
+// the row's end (256 x 16 x 4096 forward 105 -> 27 us, backward 267 -> 62).
+constexpr int kGlrShort = 16;
+typedef GlrTile<2, 32, 8, 1> GlrFwdPairShort;
+typedef GlrTile<1, 32, 8, 1> GlrFwdSingleShort;
+typedef GlrTile<2, 32, 4, 2> GlrBwdPairShort;
+typedef GlrTile<1, 32, 8, 1> GlrBwdSingleShort;
+static_assert(GlrFwdPairShort::RT == kGlrShort && GlrFwdSingleShort::RT == kGlrShort, "");
+static_assert(GlrBwdPairShort::RT == kGlrShort && GlrBwdSingleShort::RT == kGlrShort, "");
 constexpr int kGlrFwdRound = 128, kGlrBwdBlock = 64;   // tokens a forward round, a backward block
 static_assert(GlrFwdPair::RT == kGlrFwdRound && GlrFwdSingle::RT == kGlrFwdRound, "");
 static_assert(GlrBwdPair::RT == kGlrBwdBlock && GlrBwdSingle::RT == kGlrBwdBlock && GlrBlockPair::RT == kGlrBwdBlock, "");
@@ -239,23 +248,35 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
     };
     auto round = [&](int t, int buf, auto full) {
         constexpr bool FULL = decltype(full)::value;
+        // whether the wave has a token before the row's end at all: short rows
+        // leave most waves of a round without one
+        const bool any = FULL || t + __builtin_amdgcn_readfirstlane(tid / 64) * (TL::TL * T) < L;
         const uint32_t cut = PACKED ? glr_wave_resets<TL>(a.seq_idx + row, t + tid / 64 * (TL::TL * T), L) : 0u;
         float p[T][V], q[T][V];
+        if (any) {
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
+            for (int i = 0; i < T; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float k;
-                gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p[i][v], k);
-                p[i][v] = glr_mark<PACKED>(p[i][v], (cut >> i) & 1);
-                q[i][v] = k * RW::at(xr[i], v);
-                if (!FULL) {
-                    // past the row's end: the identity map
-                    const bool ok = t + m + i < L;
-                    p[i][v] = ok ? p[i][v] : 1.f;
-                    q[i][v] = ok ? q[i][v] : 0.f;
+                for (int v = 0; v < V; ++v) {
+                    float k;
+                    gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p[i][v], k);
+                    p[i][v] = glr_mark<PACKED>(p[i][v], (cut >> i) & 1);
+                    q[i][v] = k * RW::at(xr[i], v);
+                    if (!FULL) {
+                        // past the row's end: the identity map
+                        const bool ok = t + m + i < L;
+                        p[i][v] = ok ? p[i][v] : 1.f;
+                        q[i][v] = ok ? q[i][v] : 0.f;
+                    }
                 }
-            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    p[i][v] = 1.f;
+                    q[i][v] = 0.f;
+                }
         }
         // the maps are formed here, before the next loads take the registers of
         // the words they came from, and not sunk to their use behind them
@@ -264,7 +285,7 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) asm volatile("" : "+v"(p[i][v]), "+v"(q[i][v]));
         // (z in front of them: waiting for it does not wait for them)
-        if (GATE) glr_load<FULL>(zr, zb + t * a.zs, a.zs, m, cb, L - t);
+        if (GATE && any) glr_load<FULL>(zr, zb + t * a.zs, a.zs, m, cb, L - t);
         if (t + TL::RT < t1) load(t + TL::RT);
         float h[V];
 #pragma unroll
@@ -283,6 +304,7 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
         glr_enter<PACKED, TL>(h, seg_map[buf], cg * V, seg);
         const __amdgpu_buffer_rsrc_t yt = buffer_of(yb + t * ys);
         const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
+        if (any)
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             float o[V];
@@ -429,11 +451,17 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
     float dA[V], dbias[V];
     auto block = [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
+        const bool any = FULL || t + __builtin_amdgcn_readfirstlane(tid / 64) * (TL::TL * T) < L;
         R xr[T], gr[T], zr[T], dr[T];
-        glr_load<FULL>(gr, gb, a.gs, m, cb, L - t);
-        glr_load<FULL>(xr, xb, a.xs, m, cb, L - t);
-        glr_load<FULL>(dr, db, a.dys, m, cb, L - t);
-        if (GATE) glr_load<FULL>(zr, zb, a.zs, m, cb, L - t);
+        if (any) {
+            glr_load<FULL>(gr, gb, a.gs, m, cb, L - t);
+            glr_load<FULL>(xr, xb, a.xs, m, cb, L - t);
+            glr_load<FULL>(dr, db, a.dys, m, cb, L - t);
+            if (GATE) glr_load<FULL>(zr, zb, a.zs, m, cb, L - t);
+        } else {
+#pragma unroll
+            for (int i = 0; i < T; ++i) xr[i] = gr[i] = zr[i] = dr[i] = R{};
+        }
         const uint32_t cut = PACKED ? glr_wave_resets<TL>(a.seq_idx + row, t + tid / 64 * (TL::TL * T), L) : 0u;
         float A[V], bias[V];
 #pragma unroll
@@ -445,20 +473,30 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
         // decay, input factor, softplus (base 2) and its derivative, the
         // gate's sigmoid; past the row's end the identity
         float al[T][V], k[T][V], sp[T][V], sg[T][V], sz[T][V];
+        if (any) {
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+            for (int i = 0; i < T; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float gv = RW::at(gr[i], v) + bias[v];
-                float e, o;
-                const float s = softplus2(gv, e, o), l = A[v] * s;
-                const float av = __builtin_amdgcn_exp2f(l);
-                al[i][v] = ok(i) ? av : 1.f;
-                k[i][v] = ok(i) ? (NORM ? __builtin_amdgcn_sqrtf(one_minus_square(av, l)) : 1.f) : 0.f;
-                sp[i][v] = ok(i) ? s : 0.f;
-                sg[i][v] = ok(i) ? (gv >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(o) : 0.f;
-                if (GATE) sz[i][v] = sigmoid_f32(RW::at(zr[i], v));
-            }
+                for (int v = 0; v < V; ++v) {
+                    const float gv = RW::at(gr[i], v) + bias[v];
+                    float e, o;
+                    const float s = softplus2(gv, e, o), l = A[v] * s;
+                    const float av = __builtin_amdgcn_exp2f(l);
+                    al[i][v] = ok(i) ? av : 1.f;
+                    k[i][v] = ok(i) ? (NORM ? __builtin_amdgcn_sqrtf(one_minus_square(av, l)) : 1.f) : 0.f;
+                    sp[i][v] = ok(i) ? s : 0.f;
+                    sg[i][v] = ok(i) ? (gv >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(o) : 0.f;
+                    if (GATE) sz[i][v] = sigmoid_f32(RW::at(zr[i], v));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    al[i][v] = 1.f;
+                    k[i][v] = sp[i][v] = sg[i][v] = sz[i][v] = 0.f;
+                }
+        }
         auto p_of = [&](int i, int v) { return glr_mark<PACKED>(al[i][v], (cut >> i) & 1); };
         auto e_of = [&](int i, int v) {
             const float d = RW::at(dr[i], v);
@@ -480,12 +518,15 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
         }
         __syncthreads();
         // the segments are joined by a thread per channel and direction, which
-        // costs a barrier and spares each lane the maps on both its sides
+        // costs a barrier and spares each lane the maps on both its sides; a row
+        // of one block starts from init and dfinal
+        static_assert(2 * CT <= TL::W * 64, "a thread per channel and direction");
         if (tid < 2 * CT && u.ct * CT + tid % CT < D) {
             const int ch = tid % CT;
             const int64_t at = ((int64_t)u.b * a.nblk + u.blk) * D + u.ct * CT + ch;
+            const float *h0 = a.nblk > 1 ? a.ws_h : a.init, *e0 = a.nblk > 1 ? a.ws_e : a.dfinal;
             if (tid < CT) {
-                float hv = a.ws_h[at];
+                float hv = h0 ? h0[at] : 0.f;
 #pragma unroll 4
                 for (int s = 0; s < SEG; ++s) {
                     const float2 f = seg_map[s][ch];
@@ -493,13 +534,14 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
                     hv = glr_apply<PACKED>(f.x, hv, f.y);
                 }
             } else {
-                float ev = a.ws_e[at];
+                float ev = e0 ? e0[at] : 0.f;
 #pragma unroll 4
                 for (int s = SEG - 1; s >= 0; --s) {
                     const float p = seg_map[s][ch].x, own = seg_e[s][ch];
                     seg_e[s][ch] = ev;
                     ev = glr_apply<PACKED>(p, ev, own);
                 }
+                if (a.nblk == 1 && a.dinit) a.dinit[at] = ev;
             }
         }
         __syncthreads();
@@ -524,6 +566,7 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
         const __amdgpu_buffer_rsrc_t og = buffer_of((char *)a.dg + (row + t) * ys);
         const __amdgpu_buffer_rsrc_t oz = buffer_of((char *)a.dz + (row + t) * ys);
         const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
+        if (any)
 #pragma unroll
         for (int i = T - 1; i >= 0; --i) {
             float dx[V], dg[V], dz[V];
@@ -607,10 +650,12 @@ void launch_glr_block_scan(const GlrArgs &a, hipStream_t stream);
 
 template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
 void launch_glr_bwd_gate(const GlrArgs &a, hipStream_t stream) {
-    typedef typename std::conditional<TL::V == 2, GlrBlockPair, TL>::type BL;
-    hipLaunchKernelGGL((glr_block_kernel<IO, BL, NORM, PACKED, true, GATE>), glr_grid<BL>(a, a.nblk), dim3(BL::W * 64),
-                       0, stream, a, a.nblk);
-    launch_glr_block_scan(a, stream);
+    typedef typename std::conditional<TL::V == 2, GlrBlockPair, GlrBwdSingle>::type BL;
+    if (a.nblk > 1) {
+        hipLaunchKernelGGL((glr_block_kernel<IO, BL, NORM, PACKED, true, GATE>), glr_grid<BL>(a, a.nblk),
+                           dim3(BL::W * 64), 0, stream, a, a.nblk);
+        launch_glr_block_scan(a, stream);
+    }
     hipLaunchKernelGGL((glr_bwd_kernel<IO, TL, NORM, PACKED, GATE>), glr_grid<TL>(a, a.nblk), dim3(TL::W * 64), 0,
                        stream, a);
 }
@@ -626,24 +671,34 @@ void launch_glr_bwd_tile(const GlrArgs &a, hipStream_t stream) {
     a.seq_idx ? launch_glr_bwd_docs<IO, TL, NORM, true>(a, stream) : launch_glr_bwd_docs<IO, TL, NORM, false>(a, stream);
 }
 
-#define SSD_GLR_INSTANTIATE(IO)                                                                      \
-    template <>                                                                                      \
-    void launch_glr_fwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                    \
-        if (pair)                                                                                    \
-            a.normalize ? launch_glr_fwd_tile<IO, GlrFwdPair, true>(a, stream)                          \
-                        : launch_glr_fwd_tile<IO, GlrFwdPair, false>(a, stream);                        \
-        else                                                                                         \
-            a.normalize ? launch_glr_fwd_tile<IO, GlrFwdSingle, true>(a, stream)                        \
-                        : launch_glr_fwd_tile<IO, GlrFwdSingle, false>(a, stream);                      \
-    }                                                                                                \
-    template <>                                                                                      \
-    void launch_glr_bwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                    \
-        if (pair)                                                                                    \
-            a.normalize ? launch_glr_bwd_tile<IO, GlrBwdPair, true>(a, stream)                          \
-                        : launch_glr_bwd_tile<IO, GlrBwdPair, false>(a, stream);                        \
-        else                                                                                         \
-            a.normalize ? launch_glr_bwd_tile<IO, GlrBwdSingle, true>(a, stream)                        \
-                        : launch_glr_bwd_tile<IO, GlrBwdSingle, false>(a, stream);                      \
+template <typename IO, bool NORM>
+void launch_glr_fwd_len(bool pair, const GlrArgs &a, hipStream_t stream) {
+    const bool brief = a.seqlen <= kGlrShort;
+    if (pair)
+        brief ? launch_glr_fwd_tile<IO, GlrFwdPairShort, NORM>(a, stream) : launch_glr_fwd_tile<IO, GlrFwdPair, NORM>(a, stream);
+    else
+        brief ? launch_glr_fwd_tile<IO, GlrFwdSingleShort, NORM>(a, stream)
+              : launch_glr_fwd_tile<IO, GlrFwdSingle, NORM>(a, stream);
+}
+
+template <typename IO, bool NORM>
+void launch_glr_bwd_len(bool pair, const GlrArgs &a, hipStream_t stream) {
+    const bool brief = a.seqlen <= kGlrShort;
+    if (pair)
+        brief ? launch_glr_bwd_tile<IO, GlrBwdPairShort, NORM>(a, stream) : launch_glr_bwd_tile<IO, GlrBwdPair, NORM>(a, stream);
+    else
+        brief ? launch_glr_bwd_tile<IO, GlrBwdSingleShort, NORM>(a, stream)
+              : launch_glr_bwd_tile<IO, GlrBwdSingle, NORM>(a, stream);
+}
+
+#define SSD_GLR_INSTANTIATE(IO)                                                                                     \
+    template <>                                                                                                     \
+    void launch_glr_fwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                                   \
+        a.normalize ? launch_glr_fwd_len<IO, true>(pair, a, stream) : launch_glr_fwd_len<IO, false>(pair, a, stream); \
+    }                                                                                                               \
+    template <>                                                                                                     \
+    void launch_glr_bwd_io<IO>(bool pair, const GlrArgs &a, hipStream_t stream) {                                   \
+        a.normalize ? launch_glr_bwd_len<IO, true>(pair, a, stream) : launch_glr_bwd_len<IO, false>(pair, a, stream); \
     }
 
 }  // namespace ssd

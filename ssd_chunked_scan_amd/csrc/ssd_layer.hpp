@@ -26,7 +26,8 @@ struct GlrArgs {
     float *dA, *dbias, *dinit;      // backward; dbias, dinit nullable
     // Per (row, block, channel): the block's decay product, its end state from
     // a zero start, and (backward) the adjoint it passes on from a zero one.
-    // The block scan replaces the latter two by the entering values.
+    // The block scan replaces the latter two by the entering values.  Unused
+    // for a row of one block.
     float *ws_p, *ws_h, *ws_e;      // [batch][nblk][channels]
     float *part;                    // [batch * nblk][2][channels]: dA, dbias of each block
     int batch, seqlen, channels;

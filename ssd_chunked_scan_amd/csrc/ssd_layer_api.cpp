@@ -139,8 +139,9 @@ ssd_status_t check_glr(const ssd_glr_shape_t *s, ssd_dtype_t io) {
     SSD_TRY(check_reserved(s->reserved));
     // the smallest strip is 32 channels
     const int64_t units = s->batch * ((s->seqlen + kBlock - 1) / kBlock) * ((s->channels + 31) / 32);
-    // (the block scan takes 1024 threads for every 64 channels of a row)
-    if (units > kMaxGrid || s->batch * ((s->channels + 63) / 64) > kMaxThreads / 1024)
+    // (workgroups of up to 512 threads; the block scan takes 1024 for every 64
+    // channels of a row)
+    if (units > kMaxThreads / 512 || s->batch * ((s->channels + 63) / 64) > kMaxThreads / 1024)
         return fail(SSD_ERR_UNSUPPORTED, "problem too large: %lld work units", (long long)units);
     return SSD_OK;
 }

@@ -170,19 +170,22 @@ def _workspace(given, need: int, device):
     return given
 
 
-def _outputs(given, wanted, device):
-    """The dict of a backward pass's outputs: new ones, or those given for
-    every wanted entry; None where nothing is wanted."""
+def _outputs(given, wanted, dinit_type=None):
+    """The dict of a backward pass's outputs, each of the shape and type of the
+    tensor named for it (dinit of dinit_type): new ones, or those given; None
+    where that is None."""
     out = {}
-    for name, spec in wanted.items():
-        if spec is None:
+    for name, like in wanted.items():
+        if like is None:
             out[name] = None
-        elif given is None:
-            out[name] = torch.empty(spec[0], dtype=spec[1], device=device)
+            continue
+        dtype = dinit_type if name == "dinit" and dinit_type is not None else like.dtype
+        if given is None:
+            out[name] = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         else:
             if given.get(name) is None:
                 raise ValueError(f"out: {name} is missing")
-            _dense(given[name], name, spec[0], spec[1], device)
+            _dense(given[name], name, like.shape, dtype, like.device)
             out[name] = given[name]
     return out
 
@@ -247,11 +250,8 @@ def ssd_glr_bwd(x, g, A, bias, dy, z=None, seq_idx=None, init_states=None, dfina
     dev, b, D, f32 = x.device, shape.batch, shape.channels, torch.float32
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
     _dense(dfinal, "dfinal", (b, D), f32, dev)
-    act = (x.shape, x.dtype)
     with _On(dev, stream) as st:
-        out = _outputs(out, {"dx": act, "dg": act, "dz": None if z is None else act, "dA": ((D,), f32),
-                             "dbias": None if bias is None else ((D,), f32),
-                             "dinit": None if init_states is None else ((b, D), f32)}, dev)
+        out = _outputs(out, {"dx": x, "dg": x, "dz": z, "dA": A, "dbias": bias, "dinit": init_states})
         need = int(lib.ssd_glr_bwd_workspace_bytes(ctypes.byref(shape), io))
         ws = _workspace(workspace, need, dev)
         status = lib.ssd_glr_bwd(ctypes.byref(shape), io, x.data_ptr(), g.data_ptr(), A.data_ptr(), _ptr(bias), _ptr(z),
@@ -338,9 +338,7 @@ def ssd_conv_bwd(x, weight, bias, dy, seq_idx=None, init_states=None, dfinal=Non
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
     _dense(dfinal, "dfinal", (b, W - 1, D), f32, dev)
     with _On(dev, stream) as st:
-        out = _outputs(out, {"dx": (x.shape, x.dtype), "dweight": ((D, W), f32),
-                             "dbias": None if bias is None else ((D,), f32),
-                             "dinit": None if init_states is None else ((b, W - 1, D), f32)}, dev)
+        out = _outputs(out, {"dx": x, "dweight": weight, "dbias": bias, "dinit": init_states}, f32)
         need = int(lib.ssd_conv_bwd_workspace_bytes(ctypes.byref(shape), io))
         ws = _workspace(workspace, need, dev)
         status = lib.ssd_conv_bwd(ctypes.byref(shape), io, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(seq_idx),
@@ -428,7 +426,10 @@ def ssd_norm_quant_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5,
     per = shape.columns // ngroups if ngroups > 0 else 0
     blocks = -(-per // block) if block > 0 else 1
     with _On(x.device, stream) as st:
-        q = _output(q, "q", x.shape, torch.float8_e4m3fn, x.device)
+        if q is None:
+            q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        else:
+            _dense(q, "q", x.shape, torch.float8_e4m3fn, x.device)
         scales = _output(scales, "scales", (*x.shape[:-1], max(ngroups, 0) * blocks), torch.float32, x.device)
         if residual is not None:
             residual_out = _like(residual_out, "residual_out", x)
@@ -452,10 +453,8 @@ def ssd_norm_bwd(x, weight, dy, z=None, dresidual=None, eps: float = 1e-5, ngrou
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
     if dresidual is not None:
         shape.dresidual_stride = _tokens(dresidual, "dresidual", x.shape, x.dtype, dev)
-    act = (x.shape, x.dtype)
     with _On(dev, stream) as st:
-        out = _outputs(out, {"dx": act, "dz": None if z is None else act,
-                             "dweight": None if weight is None else ((x.shape[-1],), torch.float32)}, dev)
+        out = _outputs(out, {"dx": x, "dz": z, "dweight": weight})
         need = int(lib.ssd_norm_bwd_workspace_bytes(ctypes.byref(shape), io)) if weight is not None else 0
         ws = _workspace(workspace, need, dev)
         status = lib.ssd_norm_bwd(ctypes.byref(shape), io, x.data_ptr(), _ptr(weight), _ptr(z), dy.data_ptr(),

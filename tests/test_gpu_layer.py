@@ -215,6 +215,28 @@ def test_glr_splits_at_every_length():
         within(f"final at {L}", final, rf, io)
 
 
+@pytest.mark.parametrize("D", [34, 33])
+@pytest.mark.parametrize("L", [15, 16, 17, 31, 63, 64, 65])
+def test_glr_around_the_tiles(L, D):
+    """Rows of just under, exactly and just over a tile's tokens."""
+    io, s, grad = glr_inputs((3, L, D, "f32", True, True, 9, True, None), seed=L)
+    y, final = ssd.ssd_glr_fwd(**s)
+    r = glr_reference(s)
+    within("y", y, r.outputs()[0], io)
+    within("final", final, r.outputs()[1], io)
+    got = ssd.ssd_glr_bwd(**s, **grad)
+    want = r.backward(cpu(grad["dy"]), cpu(grad["dfinal"]))
+    for k in want:
+        within(k, got[k], want[k], io)
+    # and without the states at either end
+    s["init_states"] = None
+    got = ssd.ssd_glr_bwd(**s, dy=grad["dy"])
+    want = glr_reference(s).backward(cpu(grad["dy"]), None)
+    assert got["dinit"] is None
+    for k in ("dx", "dg", "dz", "dA", "dbias"):
+        within(k, got[k], want[k], io)
+
+
 def directional(J, grads, inputs, gen):
     """<grad, d> against a central difference of J along d, in fp32 outputs
     summed in fp64."""
