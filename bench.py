@@ -340,6 +340,86 @@ def backward_bench(wl, inp, args):
         "p10_us": ms[len(ms) // 10] * 1e3, "p90_us": ms[(9 * len(ms)) // 10] * 1e3}), flush=True)
 
 
+def layer_bench(wl, inp, args):
+    """One JSON line: the operators of a layer around the scan at the
+    workload's sizes, each timed per launch with HIP events on its stream.  The
+    layer reads a residual stream of half the inner width, norms it, and takes
+    z | x | B | C | dt from one projection's rows (the two projections are the
+    caller's and not timed): convolution of x, B and C out of those rows,
+    ssd_fwd, the gated norm; the gated linear recurrence in the scan's place;
+    their backward passes; and the single-token forms.  GB/s counts each
+    operator's inputs and outputs once."""
+    import torch
+    import ssd_chunked_scan_amd as ssd
+    dev = torch.device("cuda:0")
+    io = torch.bfloat16 if wl.io == "bf16" else torch.float32
+    e = 2 if wl.io == "bf16" else 4
+    b, L, H, P, N, G = wl.batch, wl.seqlen, wl.nheads, wl.headdim, wl.dstate, wl.ngroups
+    D, S, W = H * P, H * P // 2, 4
+    gen = torch.Generator(device=dev).manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=gen, device=dev, dtype=torch.float32)
+    t = lambda a, d=torch.float32: torch.from_numpy(a).to(dev).to(d).contiguous()
+    seq = None if inp.seq_idx is None else torch.from_numpy(inp.seq_idx).to(dev)
+    hidden, stream = r(b, L, S).to(io), r(b, L, S).to(io)
+    row = 2 * D + 2 * G * N + H
+    proj = r(b, L, row).to(io)
+    z, x = proj[..., :D], proj[..., D:2 * D]
+    B, C = proj[..., 2 * D:2 * D + G * N], proj[..., 2 * D + G * N:2 * D + 2 * G * N]
+    dt, A, skip = t(inp.dt), t(inp.A), t(inp.D)
+    wx, wb, wc = 0.5 * r(D, W), 0.5 * r(G * N, W), 0.5 * r(G * N, W)
+    cb, nw, sw = 0.1 * r(D), 1 + 0.1 * r(D), 1 + 0.1 * r(S)
+    gA, gb = -1 - r(D).abs(), r(D) - 4
+    xc, Bc, Cc = (ssd.ssd_conv_fwd(a, w, seq_idx=seq)[0] for a, w in ((x, wx), (B, wb), (C, wc)))
+    y = ssd.ssd_fwd(xc.view(b, L, H, P), dt, A, Bc.view(b, L, G, N), Cc.view(b, L, G, N), skip, seq,
+                    chunk_size=wl.chunk_size)[0].view(b, L, D)
+    gate = r(b, L, D).to(io)
+    dy, ds = r(b, L, D).to(io), r(b, L, S).to(io)
+    tok = proj[:, 0]
+    window = torch.zeros(b, W - 1, D, dtype=io, device=dev)
+    state = torch.zeros(b, D, device=dev)
+    n, m = b * L * D * e, b * L * S * e
+    runs = {
+        "norm_residual": (lambda: ssd.ssd_norm_fwd(hidden, sw, residual=stream), 4 * m),
+        "norm_residual_8bit": (lambda: ssd.ssd_norm_quant_fwd(hidden, sw, residual=stream), 3 * m + m // e),
+        "conv_x": (lambda: ssd.ssd_conv_fwd(x, wx, bias=cb, seq_idx=seq), 2 * n),
+        "conv_B_and_C": (lambda: (ssd.ssd_conv_fwd(B, wb, seq_idx=seq), ssd.ssd_conv_fwd(C, wc, seq_idx=seq)),
+                         4 * b * L * G * N * e),
+        "ssd_fwd": (lambda: ssd.ssd_fwd(xc.view(b, L, H, P), dt, A, Bc.view(b, L, G, N), Cc.view(b, L, G, N), skip, seq,
+                                        chunk_size=wl.chunk_size), wl.algorithmic_bytes()),
+        "gated_norm": (lambda: ssd.ssd_norm_fwd(y, nw, z=z, ngroups=G), 3 * n),
+        "glr_fwd": (lambda: ssd.ssd_glr_fwd(xc, gate, gA, bias=gb, z=z, seq_idx=seq), 4 * n),
+        "glr_bwd": (lambda: ssd.ssd_glr_bwd(xc, gate, gA, gb, dy, z=z, seq_idx=seq), 7 * n),
+        "conv_x_bwd": (lambda: ssd.ssd_conv_bwd(x, wx, cb, dy, seq_idx=seq), 3 * n),
+        "gated_norm_bwd": (lambda: ssd.ssd_norm_bwd(y, nw, dy, z=z, ngroups=G), 5 * n),
+        "norm_residual_bwd": (lambda: ssd.ssd_norm_bwd(hidden, sw, ds, dresidual=stream), 4 * m),
+        "conv_x_step": (lambda: ssd.ssd_conv_step(tok[:, D:2 * D], wx, window, bias=cb), 8 * b * D * e),
+        "glr_step": (lambda: ssd.ssd_glr_step(tok[:, D:2 * D], gate[:, 0], gA, state, bias=gb, z=tok[:, :D]),
+                     b * D * (4 * e + 8)),
+    }
+    cuda_stream = torch.cuda.current_stream(dev)
+    out = {}
+    for name, (run, nbytes) in runs.items():
+        for _ in range(max(args.warmup, 1)):
+            run()
+        torch.cuda.synchronize(dev)
+        ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)) for _ in range(args.steps)]
+        for e0, e1 in ev:
+            e0.record(cuda_stream)
+            run()
+            e1.record(cuda_stream)
+        torch.cuda.synchronize(dev)
+        us = sorted(e0.elapsed_time(e1) * 1e3 for e0, e1 in ev)
+        avg = sum(us) / len(us)
+        gbs = nbytes / (avg * 1e-6) / 1e9
+        out[name] = {"us": avg, "median_us": us[len(us) // 2], "bytes": nbytes, "gbs": gbs, "frac": gbs / HBM_PEAK_GBS}
+        print(f"bench: {name}: {avg:.1f} us, {gbs:.0f} GB/s", file=sys.stderr, flush=True)
+    print(json.dumps({"metric": "time per launch of a layer's operators around the scan", "unit": "us",
+                      "higher_is_better": False, "steps": args.steps, "warmup": args.warmup, "dtype": wl.io,
+                      "data": "synthetic", "operators": out,
+                      "config": {"workload": wl.name, "batch": b, "seqlen": L, "inner_width": D, "stream_width": S,
+                                 "conv_width": W, "dstate": N, "ngroups": G}}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -356,6 +436,9 @@ def main():
                          "head kernel (chunk 256) and in the mask export alone")
     ap.add_argument("--backward", action="store_true",
                     help="instead of the forward pass: time the backward pass (ssd_bwd)")
+    ap.add_argument("--layer", action="store_true",
+                    help="instead of the forward pass: time the operators of a layer around it "
+                         "(norms, convolution, gated linear recurrence; forward, backward, one token)")
     ap.add_argument("--flush", choices=["write", "read"], default="read",
                     help="how the caches are emptied before each cold call: write a 512 MiB scratch "
                          "buffer (also leaves dirty lines to write back), or read one")
@@ -390,6 +473,9 @@ def main():
         return
     if args.backward:
         backward_bench(wl, inp, args)
+        return
+    if args.layer:
+        layer_bench(wl, inp, args)
         return
     dev = torch.device("cuda:0")
     io = torch.bfloat16 if wl.io == "bf16" else torch.float32

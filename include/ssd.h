@@ -356,8 +356,9 @@ ssd_status_t ssd_fwd_noalloc(const ssd_shape_t *shape, ssd_dtype_t io,
  * of their type (16-byte aligned ones with a stride that keeps every token
  * aligned are faster).  Outputs must not overlap inputs, except that
  * residual_out may be the residual itself and a step's state is updated in
- * place.  Channels, columns and strides are at most 2^20, tokens (batch
- * seqlen, rows) at most 2^30 - 1. */
+ * place.  Channels and columns are at most 2^20, tokens (batch seqlen, rows)
+ * at most 2^30 - 1, strides at most 2^22 elements (2^40 for the norm and for
+ * rows of one token). */
 
 /* Gated linear recurrence.  Per channel c, with the same decay map and
  * document resets as ssd_fwd:

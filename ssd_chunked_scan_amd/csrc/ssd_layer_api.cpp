@@ -39,7 +39,11 @@ ssd_status_t fail(ssd_status_t st, const char *fmt, ...) {
 }
 
 constexpr int64_t kMaxTokens = ((int64_t)1 << 30) - 1;
-constexpr int64_t kMaxChannels = (int64_t)1 << 20;   // also of a stride
+constexpr int64_t kMaxChannels = (int64_t)1 << 20;
+// Strides in elements: a round of 128 tokens is addressed with 32-bit byte
+// offsets; single tokens and rows of the norm with 64-bit ones.
+constexpr int64_t kMaxStride = (int64_t)1 << 22, kMaxRowStride = (int64_t)1 << 40;
+constexpr int64_t kMaxSpan = (int64_t)1 << 60;
 constexpr int64_t kMaxThreads = 0xffffffff;          // of one launch
 constexpr int64_t kMaxGrid = kMaxThreads / 256;      // workgroups of 256 threads
 constexpr int64_t kMaxNormWidth = 16384;             // columns of a norm group: held in registers
@@ -70,12 +74,14 @@ ssd_status_t check_tokens(int64_t batch, int64_t seqlen, int64_t channels) {
     return SSD_OK;
 }
 
-// A token stride in elements (0: dense).
-ssd_status_t check_stride(const char *name, int64_t stride, int64_t channels) {
+// A token stride in elements (0: dense) of `tokens` tokens, `apart` of them in
+// one row.
+ssd_status_t check_stride(const char *name, int64_t stride, int64_t channels, int64_t tokens, int64_t apart) {
     if (stride != 0 && stride < channels)
         return fail(SSD_ERR_SHAPE, "%s_stride %lld is below the %lld elements of a token", name, (long long)stride,
                     (long long)channels);
-    if (stride > kMaxChannels) return fail(SSD_ERR_UNSUPPORTED, "%s_stride %lld is too large", name, (long long)stride);
+    if (stride > (apart > 1 ? kMaxStride : kMaxRowStride) || stride > kMaxSpan / tokens)
+        return fail(SSD_ERR_UNSUPPORTED, "%s_stride %lld is too large", name, (long long)stride);
     return SSD_OK;
 }
 
@@ -130,10 +136,10 @@ ssd_status_t check_glr(const ssd_glr_shape_t *s, ssd_dtype_t io) {
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
     SSD_TRY(check_io(io));
     SSD_TRY(check_tokens(s->batch, s->seqlen, s->channels));
-    SSD_TRY(check_stride("x", s->x_stride, s->channels));
-    SSD_TRY(check_stride("g", s->g_stride, s->channels));
-    SSD_TRY(check_stride("z", s->z_stride, s->channels));
-    SSD_TRY(check_stride("dy", s->dy_stride, s->channels));
+    SSD_TRY(check_stride("x", s->x_stride, s->channels, s->batch * s->seqlen, s->seqlen));
+    SSD_TRY(check_stride("g", s->g_stride, s->channels, s->batch * s->seqlen, s->seqlen));
+    SSD_TRY(check_stride("z", s->z_stride, s->channels, s->batch * s->seqlen, s->seqlen));
+    SSD_TRY(check_stride("dy", s->dy_stride, s->channels, s->batch * s->seqlen, s->seqlen));
     if (s->normalize != 0 && s->normalize != 1)
         return fail(SSD_ERR_UNSUPPORTED, "normalize must be 0 or 1, got %lld", (long long)s->normalize);
     SSD_TRY(check_reserved(s->reserved));
@@ -197,8 +203,8 @@ ssd_status_t check_conv(const ssd_conv_shape_t *s, ssd_dtype_t io) {
     SSD_TRY(check_io(io));
     SSD_TRY(check_tokens(s->batch, s->seqlen, s->channels));
     if (s->width < 2 || s->width > 4) return fail(SSD_ERR_UNSUPPORTED, "width %lld not in {2, 3, 4}", (long long)s->width);
-    SSD_TRY(check_stride("x", s->x_stride, s->channels));
-    SSD_TRY(check_stride("dy", s->dy_stride, s->channels));
+    SSD_TRY(check_stride("x", s->x_stride, s->channels, s->batch * s->seqlen, s->seqlen));
+    SSD_TRY(check_stride("dy", s->dy_stride, s->channels, s->batch * s->seqlen, s->seqlen));
     if (s->silu != 0 && s->silu != 1) return fail(SSD_ERR_UNSUPPORTED, "silu must be 0 or 1, got %lld", (long long)s->silu);
     SSD_TRY(check_reserved(s->reserved));
     // single channels: a wave per 16 tokens x 64 channels (forward), a workgroup
@@ -248,11 +254,11 @@ ssd_status_t check_norm(const ssd_norm_shape_t *s, ssd_dtype_t io, bool quant) {
         return fail(SSD_ERR_UNSUPPORTED, "a norm group has %lld columns, at most %lld are supported",
                     (long long)(s->columns / s->ngroups), (long long)kMaxNormWidth);
     if (s->ngroups > 65535) return fail(SSD_ERR_UNSUPPORTED, "ngroups %lld is too large", (long long)s->ngroups);
-    SSD_TRY(check_stride("x", s->x_stride, s->columns));
-    SSD_TRY(check_stride("z", s->z_stride, s->columns));
-    SSD_TRY(check_stride("residual", s->residual_stride, s->columns));
-    SSD_TRY(check_stride("dy", s->dy_stride, s->columns));
-    SSD_TRY(check_stride("dresidual", s->dresidual_stride, s->columns));
+    SSD_TRY(check_stride("x", s->x_stride, s->columns, s->rows, 1));
+    SSD_TRY(check_stride("z", s->z_stride, s->columns, s->rows, 1));
+    SSD_TRY(check_stride("residual", s->residual_stride, s->columns, s->rows, 1));
+    SSD_TRY(check_stride("dy", s->dy_stride, s->columns, s->rows, 1));
+    SSD_TRY(check_stride("dresidual", s->dresidual_stride, s->columns, s->rows, 1));
     if (!(std::isfinite(s->eps) && s->eps > 0.f)) return fail(SSD_ERR_UNSUPPORTED, "eps must be positive and finite");
     if (s->quant_block != 0 && !(quant && s->quant_block == 128))
         return fail(SSD_ERR_UNSUPPORTED, "quant_block %d: 0 or 128, and 0 without an 8-bit output", (int)s->quant_block);

@@ -646,6 +646,32 @@ def test_offsets_past_32_bits():
     assert torch.equal(n1["dx"], n2["dx"])
 
 
+def test_single_tokens_far_apart():
+    """One token of each row of a long, wide buffer."""
+    gen = torch.Generator().manual_seed(10)
+    b, L, W, D = 3, 2000, 6000, 64
+    wide = torch.zeros(b, L, W, dtype=torch.bfloat16, device=DEV)
+    x, g, z = (rand(gen, b, D, dtype=torch.bfloat16) for _ in range(3))
+    for i, t in enumerate((x, g, z)):
+        wide[:, 7, i * D:(i + 1) * D] = t
+    xs, gs, zs = (wide[:, 7, i * D:(i + 1) * D] for i in range(3))
+    A, bias = -1 - rand(gen, D).abs(), rand(gen, D) - 2
+    s1, s2 = (torch.ones(b, D, device=DEV) for _ in range(2))
+    assert torch.equal(ssd.ssd_glr_step(xs, gs, A, s1, bias=bias, z=zs), ssd.ssd_glr_step(x, g, A, s2, bias=bias, z=z))
+    assert torch.equal(s1, s2)
+    seq = lambda t: t[:, None]
+    assert torch.equal(ssd.ssd_glr_fwd(seq(xs), seq(gs), A, bias=bias)[0], ssd.ssd_glr_fwd(seq(x), seq(g), A, bias=bias)[0])
+    w = rand(gen, D, 4)
+    c1, c2 = (torch.ones(b, 3, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert torch.equal(ssd.ssd_conv_step(xs, w, c1), ssd.ssd_conv_step(x, w, c2)) and torch.equal(c1, c2)
+    assert torch.equal(ssd.ssd_conv_fwd(seq(xs), w)[0], ssd.ssd_conv_fwd(seq(x), w)[0])
+    d1, d2 = ssd.ssd_conv_bwd(seq(xs), w, None, seq(gs)), ssd.ssd_conv_bwd(seq(x), w, None, seq(g))
+    assert torch.equal(d1["dx"], d2["dx"]) and torch.equal(d1["dweight"], d2["dweight"])
+    g1, g2 = ssd.ssd_glr_bwd(seq(xs), seq(gs), A, bias, seq(zs)), ssd.ssd_glr_bwd(seq(x), seq(g), A, bias, seq(z))
+    assert all(torch.equal(g1[k], g2[k]) for k in ("dx", "dg", "dA", "dbias"))
+    assert torch.equal(ssd.ssd_norm_fwd(xs, None, z=zs)[0], ssd.ssd_norm_fwd(x, None, z=z)[0])
+
+
 # -------------------------------------------------------------- refusals
 
 

@@ -121,7 +121,7 @@ def put(args, **kw):
     (dict(batch=0), SHAPE), (dict(seqlen=0), SHAPE), (dict(channels=-1), SHAPE),
     (dict(channels=(1 << 20) + 1), UNSUPPORTED), (dict(seqlen=1 << 30), UNSUPPORTED),
     (dict(batch=1 << 20, seqlen=1 << 20), UNSUPPORTED), (dict(batch=1 << 62), UNSUPPORTED),
-    (dict(x_stride=63), SHAPE), (dict(g_stride=-64), SHAPE), (dict(z_stride=(1 << 20) + 1), UNSUPPORTED),
+    (dict(x_stride=63), SHAPE), (dict(g_stride=-64), SHAPE), (dict(z_stride=(1 << 22) + 1), UNSUPPORTED),
     (dict(dy_stride=1), SHAPE), (dict(normalize=2), UNSUPPORTED), (dict(reserved=(ctypes.c_int64 * 4)(0, 0, 0, 1)), UNSUPPORTED),
     (dict(batch=(1 << 30) - 1, seqlen=1, channels=1 << 20), UNSUPPORTED),
 ])
@@ -151,6 +151,18 @@ def test_glr_pointers(name, args, ws, status):
     assert call(name, glr(), *args, ws=ws) == status
 
 
+def test_strides_of_single_tokens():
+    """A step reads one token of each row of a long buffer: its stride may be
+    anything that 64 bits address."""
+    far = 1 << 40
+    assert call("ssd_glr_step", glr(seqlen=1, x_stride=far, g_stride=far), *put(GLR_STEP, _0=None)) == NULL
+    assert call("ssd_glr_step", glr(seqlen=1, x_stride=far + 1), *GLR_STEP) == UNSUPPORTED
+    assert call("ssd_glr_step", glr(seqlen=1, batch=1 << 24, x_stride=far), *GLR_STEP) == UNSUPPORTED
+    assert call("ssd_conv_step", conv(seqlen=1, x_stride=far), *put(CONV_STEP, _0=None)) == NULL
+    assert call("ssd_norm_fwd", norm(x_stride=far), *put(NORM_FWD, _0=None)) == NULL
+    assert call("ssd_norm_fwd", norm(rows=1 << 21, x_stride=far), *NORM_FWD) == UNSUPPORTED
+
+
 def test_glr_split_needs_its_workspace():
     s = glr(batch=1, seqlen=4096)
     lib = ssd.load_library()
@@ -163,7 +175,7 @@ def test_glr_split_needs_its_workspace():
 
 @pytest.mark.parametrize("change,status", [
     (dict(batch=0), SHAPE), (dict(channels=0), SHAPE), (dict(width=1), UNSUPPORTED), (dict(width=5), UNSUPPORTED),
-    (dict(silu=-1), UNSUPPORTED), (dict(x_stride=10), SHAPE), (dict(dy_stride=1 << 21), UNSUPPORTED),
+    (dict(silu=-1), UNSUPPORTED), (dict(x_stride=10), SHAPE), (dict(dy_stride=(1 << 22) + 1), UNSUPPORTED),
     (dict(seqlen=1 << 31), UNSUPPORTED), (dict(reserved=(ctypes.c_int64 * 4)(1, 0, 0, 0)), UNSUPPORTED),
 ])
 def test_conv_shapes(change, status):
