@@ -40,6 +40,7 @@ struct GlrTile {
 // and for pointers that do not allow pairs.  The backward tiles hold half as
 // many tokens a lane, since seven values of each stay in registers.
 typedef GlrTile<2, 32, 8, 8> GlrFwdPair;
+typedef GlrTile<2, 16, 4, 8> GlrFwdHalf;   // half a strip for the last, partial round of workgroups
 typedef GlrTile<1, 32, 16, 4> GlrFwdSingle;
 typedef GlrTile<2, 32, 4, 8> GlrBwdPair;
 typedef GlrTile<1, 32, 8, 4> GlrBwdSingle;
@@ -54,7 +55,8 @@ typedef GlrTile<1, 32, 8, 1> GlrBwdSingleShort;
 static_assert(GlrFwdPairShort::RT == kGlrShort && GlrFwdSingleShort::RT == kGlrShort, "");
 static_assert(GlrBwdPairShort::RT == kGlrShort && GlrBwdSingleShort::RT == kGlrShort, "");
 constexpr int kGlrFwdRound = 128, kGlrBwdBlock = 64;   // tokens a forward round, a backward block
-static_assert(GlrFwdPair::RT == kGlrFwdRound && GlrFwdSingle::RT == kGlrFwdRound, "");
+static_assert(GlrFwdHalf::CT * 2 == GlrFwdPair::CT && GlrFwdHalf::W == GlrFwdPair::W, "");
+static_assert(GlrFwdHalf::RT == kGlrFwdRound && GlrFwdPair::RT == kGlrFwdRound && GlrFwdSingle::RT == kGlrFwdRound, "");
 static_assert(GlrBwdPair::RT == kGlrBwdBlock && GlrBwdSingle::RT == kGlrBwdBlock && GlrBlockPair::RT == kGlrBwdBlock, "");
 
 constexpr float kGlrReset = -0.f;
@@ -182,13 +184,12 @@ __device__ inline void glr_enter(float (&h)[TL::V], const float2 (&maps)[TL::SEG
 // composes the segments before its own.  x and g of the next round are loaded
 // as soon as this round's are used up.
 template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
-__global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
+__device__ inline void glr_fwd_walk(const GlrArgs &a, const GlrUnit u) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
     typedef Raw<IO, V> RW;
     typedef typename RW::type R;
     __shared__ float2 seg_map[2][SEG][CT];
     __shared__ float carry[2][CT];
-    const GlrUnit u = glr_unit<TL>(a, a.nblk);
     const int tid = threadIdx.x, cg = tid % TL::CL, seg = tid / TL::CL, m = seg * T;
     const int D = a.channels, L = a.seqlen;
     const int c = u.ct * CT + cg * V;
@@ -334,6 +335,37 @@ __global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
     if ((u.ct + 1) * CT <= D)
         for (; t < t1 && t + TL::RT <= L; t += TL::RT, buf ^= 1) round(t, buf, std::true_type{});
     for (; t < t1; t += TL::RT, buf ^= 1) round(t, buf, std::false_type{});
+}
+
+// A compute unit's vector unit is what its workgroups wait for, so their count
+// per compute unit should be even: with a little over one workgroup for each,
+// those left over run as two of half a strip (4 x 2048 x 5120, 320 units on 256
+// compute units: 108 -> 85 us).  Not from two for each on, where two already
+// overlap and the half strips' 64-byte rows cost more than the balance gains
+// (8 x 2048 x 5120, 640 units: 155 us whole, 160 with 128 of them halved).
+template <typename IO, typename TL, typename HALF, bool NORM, bool PACKED, bool GATE>
+__global__ __launch_bounds__(TL::W * 64) void glr_fwd_kernel(GlrArgs a) {
+    const int blk = blockIdx.x;
+    int unit;
+    if (blk < a.whole)
+        unit = xcd_contiguous(blk, a.whole);
+    else
+        unit = a.whole * 2 + xcd_contiguous(blk - a.whole, gridDim.x - a.whole);
+    const int half = blk < a.whole ? 0 : unit & 1;
+    if (blk >= a.whole) unit = (unit >> 1);
+    const int nct = (a.channels + TL::CT - 1) / TL::CT;
+    GlrUnit u;
+    u.ct = unit % nct;
+    u.blk = (unit / nct) % a.nblk;
+    u.b = unit / nct / a.nblk;
+    if constexpr (!std::is_same<TL, HALF>::value) {
+        if (blk >= a.whole) {
+            u.ct = 2 * u.ct + half;
+            if (u.ct * HALF::CT < a.channels) glr_fwd_walk<IO, HALF, NORM, PACKED, GATE>(a, u);
+            return;
+        }
+    }
+    glr_fwd_walk<IO, TL, NORM, PACKED, GATE>(a, u);
 }
 
 // The map of each block of blk_len tokens (ws_p, ws_h), and with BWD the
@@ -630,15 +662,20 @@ inline dim3 glr_grid(const GlrArgs &a, int nblk) {
 }
 
 template <typename IO, typename TL, bool NORM, bool PACKED>
-void launch_glr_fwd_docs(const GlrArgs &a, hipStream_t stream) {
+void launch_glr_fwd_docs(GlrArgs a, hipStream_t stream) {
+    typedef typename std::conditional<std::is_same<TL, GlrFwdPair>::value, GlrFwdHalf, TL>::type HALF;
     const dim3 block(TL::W * 64);
     if (a.nblk > 1)
         hipLaunchKernelGGL((glr_block_kernel<IO, TL, NORM, PACKED, false, false>), glr_grid<TL>(a, a.nblk - 1), block,
                            0, stream, a, a.nblk - 1);
+    const int units = (int)glr_grid<TL>(a, a.nblk).x;
+    a.whole = units;
+    if (!std::is_same<TL, HALF>::value && units > a.cus && 2 * units <= 3 * a.cus) a.whole = a.cus;
+    const dim3 grid((unsigned)(a.whole + 2 * (units - a.whole)));
     if (a.z)
-        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, NORM, PACKED, true>), glr_grid<TL>(a, a.nblk), block, 0, stream, a);
+        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, HALF, NORM, PACKED, true>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, NORM, PACKED, false>), glr_grid<TL>(a, a.nblk), block, 0, stream, a);
+        hipLaunchKernelGGL((glr_fwd_kernel<IO, TL, HALF, NORM, PACKED, false>), grid, block, 0, stream, a);
 }
 
 template <typename IO, typename TL, bool NORM>

@@ -33,6 +33,8 @@ struct GlrArgs {
     int batch, seqlen, channels;
     int nblk, blk_len;              // blocks (splits) per row and their tokens
     int normalize;
+    int cus;                        // forward: compute units
+    int whole;                      // forward: units that run as one workgroup, the others as two
 };
 
 struct GlrStepArgs {

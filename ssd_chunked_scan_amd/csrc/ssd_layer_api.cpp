@@ -326,6 +326,7 @@ ssd_status_t norm_fwd(const ssd_norm_shape_t *s, ssd_dtype_t io, const void *x, 
         acc.ok = acc.ok && aligned(y, n);
     else
         acc.in(y, dense);
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_norm_fwd(io == SSD_BF16, acc.ok, a, (hipStream_t)stream);
     return launched(what);
 }
@@ -357,6 +358,7 @@ ssd_status_t ssd_glr_fwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     SSD_TRY(maybe("final_states", final_states, 4));
     ssd::GlrArgs a = glr_args(shape, io, x, g, A, bias, z, seq_idx, init_states);
     glr_fwd_split(shape, (hipStream_t)stream, &a.nblk, &a.blk_len);
+    a.cus = ssd::compute_units((hipStream_t)stream);
     const size_t bytes = glr_fwd_bytes(shape, a.nblk);
     SSD_TRY(check_workspace(workspace, workspace_bytes, bytes));
     a.y = y;
@@ -365,6 +367,7 @@ ssd_status_t ssd_glr_fwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     a.ws_h = bytes ? (float *)((char *)workspace + bytes / 2) : nullptr;
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(y, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_glr_fwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_fwd");
 }
@@ -418,6 +421,7 @@ ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(dy, a.dys)
                           .in(dx, dense).in(dg, dense).in(dz, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_glr_bwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_bwd");
 }
@@ -438,6 +442,7 @@ ssd_status_t ssd_glr_step(const ssd_glr_shape_t *shape, ssd_dtype_t io, const vo
     const ssd::GlrStepArgs a = {x, g, z, s.xs, s.gs, s.zs, A, bias, state, y, s.batch, s.channels, s.normalize};
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(y, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_glr_step(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_step");
 }
@@ -460,6 +465,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(init_states, dense).in(y, dense)
                           .in(final_states, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_conv_fwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_conv_fwd");
 }
@@ -502,6 +508,7 @@ ssd_status_t ssd_conv_bwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(dy, a.dys).in(init_states, dense)
                           .in(dx, dense).ok;
     const int run = conv_run(shape, ssd::conv_strip(pair), (hipStream_t)stream);
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_conv_bwd(io == SSD_BF16, pair, a, run, dweight, dbias, (hipStream_t)stream);
     return launched("ssd_conv_bwd");
 }
@@ -521,6 +528,7 @@ ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, ssd_dtype_t io, const 
     a.y = y;
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(state, dense).in(y, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_conv_step(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_conv_step");
 }
@@ -568,6 +576,7 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_shape_t *shape, ssd_dtype_t io, const v
     const int64_t dense = shape->columns * (int64_t)e;
     const bool wide = Access(a.width % n == 0, n, io).in(x, a.xs).in(z, a.zs).in(dy, a.dys).in(dresidual, a.drs)
                           .in(dx, dense).in(dz, dense).ok;
+    (void)hipGetLastError();   // not an earlier call\'s
     ssd::launch_norm_bwd(io == SSD_BF16, wide, a, dweight, (hipStream_t)stream);
     return launched("ssd_norm_bwd");
 }
