@@ -183,6 +183,11 @@ __device__ inline void glr_enter(float (&h)[TL::V], const float2 (&maps)[TL::SEG
 // maps of its tokens, publishes its segment's map, and after one barrier
 // composes the segments before its own.  x and g of the next round are loaded
 // as soon as this round's are used up.
+//
+// Bound by vector instructions and memory alike: 44 issue slots an element for
+// the map (of them 16 in exp2, log2, exp2 and the root), 12 for the gate, 5
+// for the two passes over the tokens, in all about 133 us for 8 x 2048 x 5120
+// against 137 for its 671 MB at a large copy's rate; it takes 155 (4.3 TB/s).
 template <typename IO, typename TL, bool NORM, bool PACKED, bool GATE>
 __device__ inline void glr_fwd_walk(const GlrArgs &a, const GlrUnit u) {
     constexpr int V = TL::V, T = TL::T, SEG = TL::SEG, CT = TL::CT;
@@ -305,20 +310,21 @@ __device__ inline void glr_fwd_walk(const GlrArgs &a, const GlrUnit u) {
         glr_enter<PACKED, TL>(h, seg_map[buf], cg * V, seg);
         const __amdgpu_buffer_rsrc_t yt = buffer_of(yb + t * ys);
         const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
-        if (any)
+        if (any) {
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            float o[V];
+            for (int i = 0; i < T; ++i) {
+                float o[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = glr_apply<PACKED>(p[i][v], h[v], q[i][v]);
-                o[v] = h[v];
-                if (GATE) {
-                    const float z = RW::at(zr[i], v);
-                    o[v] *= z * sigmoid_f32(z);
+                for (int v = 0; v < V; ++v) {
+                    h[v] = glr_apply<PACKED>(p[i][v], h[v], q[i][v]);
+                    o[v] = h[v];
+                    if (GATE) {
+                        const float z = RW::at(zr[i], v);
+                        o[v] *= z * sigmoid_f32(z);
+                    }
                 }
+                if (FULL || (cok && t + m + i < L)) buffer_store<IO, V>(yt, off, (uint32_t)(i * ys), o);
             }
-            if (FULL || (cok && t + m + i < L)) buffer_store<IO, V>(yt, off, (uint32_t)(i * ys), o);
         }
         if (seg == SEG - 1) {
 #pragma unroll
@@ -455,7 +461,16 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
     }
 }
 
-// Backward, one workgroup per (row, block of RT tokens, strip), with the state
+// Backward.  The states are recomputed: first the map of every block and the
+// adjoint it passes on (glr_block_kernel: x, g, dy, z read once, 8 bytes an
+// element in bf16), joined over the row by glr_block_scan_kernel, then this
+// kernel with the same inputs again and the gradients out (14 bytes).  At 8 x
+// 2048 x 5120 with a gate 159 + 13 + 266 us, both passes at 4.2 to 4.4 TB/s
+// and at four fifths of the vector unit.  Taking the rows in groups that stay
+// in the Infinity Cache between the passes was slower (468 us in halves, 521
+// row by row): the launches' ends cost what the second reading gains.
+//
+// One workgroup per (row, block of RT tokens, strip), with the state
 // entering the block from the left (ws_h) and the adjoint from the right
 // (ws_e) already known:
 //   G_t = e_t + c_t,  c_{t-1} = p_t G_t,  e = dy [silu(z)]
@@ -598,34 +613,35 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
         const __amdgpu_buffer_rsrc_t og = buffer_of((char *)a.dg + (row + t) * ys);
         const __amdgpu_buffer_rsrc_t oz = buffer_of((char *)a.dz + (row + t) * ys);
         const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
-        if (any)
+        if (any) {
 #pragma unroll
-        for (int i = T - 1; i >= 0; --i) {
-            float dx[V], dg[V], dz[V];
+            for (int i = T - 1; i >= 0; --i) {
+                float dx[V], dg[V], dz[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float G = e_of(i, v) + cin[v];
-                const float x = RW::at(xr[i], v);
-                const bool reset = PACKED && ((cut >> i) & 1);
-                cin[v] = reset ? 0.f : al[i][v] * G;
-                dx[v] = k[i][v] * G;
-                float dla = reset ? 0.f : cin[v] * (i > 0 ? h[i > 0 ? i - 1 : 0][v] : hin[v]);
-                if (NORM) {
-                    const float rk = k[i][v] > 0.f ? __builtin_amdgcn_rcpf(k[i][v]) : 0.f;
-                    dla = fmaf(-G * x, al[i][v] * al[i][v] * rk, dla);
+                for (int v = 0; v < V; ++v) {
+                    const float G = e_of(i, v) + cin[v];
+                    const float x = RW::at(xr[i], v);
+                    const bool reset = PACKED && ((cut >> i) & 1);
+                    cin[v] = reset ? 0.f : al[i][v] * G;
+                    dx[v] = k[i][v] * G;
+                    float dla = reset ? 0.f : cin[v] * (i > 0 ? h[i > 0 ? i - 1 : 0][v] : hin[v]);
+                    if (NORM) {
+                        const float rk = k[i][v] > 0.f ? __builtin_amdgcn_rcpf(k[i][v]) : 0.f;
+                        dla = fmaf(-G * x, al[i][v] * al[i][v] * rk, dla);
+                    }
+                    dg[v] = A[v] * dla * sg[i][v];
+                    dA[v] = fmaf(sp[i][v], dla, dA[v]);
+                    dbias[v] += dg[v];
+                    if (GATE) {
+                        const float z = RW::at(zr[i], v);
+                        dz[v] = RW::at(dr[i], v) * h[i][v] * (sz[i][v] * fmaf(z, 1.f - sz[i][v], 1.f));
+                    }
                 }
-                dg[v] = A[v] * dla * sg[i][v];
-                dA[v] = fmaf(sp[i][v], dla, dA[v]);
-                dbias[v] += dg[v];
-                if (GATE) {
-                    const float z = RW::at(zr[i], v);
-                    dz[v] = RW::at(dr[i], v) * h[i][v] * (sz[i][v] * fmaf(z, 1.f - sz[i][v], 1.f));
+                if (FULL || (cok && ok(i))) {
+                    buffer_store<IO, V>(ox, off, (uint32_t)(i * ys), dx);
+                    buffer_store<IO, V>(og, off, (uint32_t)(i * ys), dg);
+                    if (GATE) buffer_store<IO, V>(oz, off, (uint32_t)(i * ys), dz);
                 }
-            }
-            if (FULL || (cok && ok(i))) {
-                buffer_store<IO, V>(ox, off, (uint32_t)(i * ys), dx);
-                buffer_store<IO, V>(og, off, (uint32_t)(i * ys), dg);
-                if (GATE) buffer_store<IO, V>(oz, off, (uint32_t)(i * ys), dz);
             }
         }
     };
