@@ -294,16 +294,24 @@ __device__ inline void glr_fwd_walk(const GlrArgs &a, const GlrUnit u) {
         if (GATE && any) glr_load<FULL>(zr, zb + t * a.zs, a.zs, m, cb, L - t);
         if (t + TL::RT < t1) load(t + TL::RT);
         float h[V];
+        // (most waves see no document start: their maps go without the marks)
+        auto chain = [&](auto marked) {
+            constexpr bool MARKED = decltype(marked)::value;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float ps = p[0][v], qs = q[0][v];
+            for (int v = 0; v < V; ++v) {
+                float ps = p[0][v], qs = q[0][v];
 #pragma unroll
-            for (int i = 1; i < T; ++i) {
-                ps = glr_join<PACKED>(ps, p[i][v]);
-                qs = glr_apply<PACKED>(p[i][v], qs, q[i][v]);
+                for (int i = 1; i < T; ++i) {
+                    ps = glr_join<MARKED>(ps, p[i][v]);
+                    qs = glr_apply<MARKED>(p[i][v], qs, q[i][v]);
+                }
+                seg_map[buf][seg][cg * V + v] = make_float2(ps, qs);
             }
-            seg_map[buf][seg][cg * V + v] = make_float2(ps, qs);
-        }
+        };
+        if (PACKED && __any(cut != 0))
+            chain(std::true_type{});
+        else
+            chain(std::false_type{});
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = carry[buf][cg * V + v];
@@ -407,6 +415,7 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
         ps[v] = 1.f;
         qs[v] = es[v] = 0.f;
     }
+    uint32_t seen = 0;
     for (int j = 0; j < per; j += T) {
         // this lane's first token: 64-bit row offsets, since a split's tokens
         // times the stride can pass 32 bits
@@ -418,27 +427,36 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
         if (BWD) glr_load_lane(dr, db + t * a.dys + cb, a.dys, L - t);
         if (BWD && GATE) glr_load_lane(zr, zb + t * a.zs + cb, a.zs, L - t);
         const uint32_t cut = PACKED ? glr_resets<T>(a.seq_idx + row, t, L) : 0u;
+        // marks only from the wave's first document start on
+        seen |= cut;
+        auto tokens = [&](auto marked) {
+            constexpr bool MARKED = decltype(marked)::value;
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            const bool ok = t + i < L;
+            for (int i = 0; i < T; ++i) {
+                const bool ok = t + i < L;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float p, k;
-                gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p, k);
-                const float q = ok ? k * RW::at(xr[i], v) : 0.f;
-                p = ok ? glr_mark<PACKED>(p, (cut >> i) & 1) : 1.f;
-                qs[v] = glr_apply<PACKED>(p, qs[v], q);
-                ps[v] = glr_join<PACKED>(ps[v], p);
-                if (BWD) {
-                    float e = RW::at(dr[i], v);
-                    if (GATE) {
-                        const float z = RW::at(zr[i], v);
-                        e *= z * sigmoid_f32(z);
+                for (int v = 0; v < V; ++v) {
+                    float p, k;
+                    gate_map<NORM>(RW::at(gr[i], v) + bias[v], A[v], p, k);
+                    const float q = ok ? k * RW::at(xr[i], v) : 0.f;
+                    p = ok ? glr_mark<PACKED>(p, MARKED && ((cut >> i) & 1)) : 1.f;
+                    qs[v] = glr_apply<MARKED>(p, qs[v], q);
+                    ps[v] = glr_join<MARKED>(ps[v], p);
+                    if (BWD) {
+                        float e = RW::at(dr[i], v);
+                        if (GATE) {
+                            const float z = RW::at(zr[i], v);
+                            e *= z * sigmoid_f32(z);
+                        }
+                        es[v] = glr_apply<MARKED>(ps[v], ok ? e : 0.f, es[v]);
                     }
-                    es[v] = glr_apply<PACKED>(ps[v], ok ? e : 0.f, es[v]);
                 }
             }
-        }
+        };
+        if (PACKED && __any(seen != 0))
+            tokens(std::true_type{});
+        else
+            tokens(std::false_type{});
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
