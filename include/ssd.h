@@ -454,7 +454,8 @@ ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, ssd_dtype_t io,
  *   v = x, or x silu(z) when z is given, or, when residual is given, the sum
  *       x + residual rounded to the io dtype (written to residual_out)
  *   y = v rsqrt(mean(v^2 over the group) + eps) weight
- * residual and z exclude each other.  Statistics in fp32. */
+ * residual and z exclude each other.  Statistics in fp32.  A group has at most
+ * 16384 columns. */
 typedef struct {
     int64_t rows, columns, ngroups;
     int64_t x_stride, z_stride, residual_stride, dy_stride, dresidual_stride; /* rows; 0 = dense */

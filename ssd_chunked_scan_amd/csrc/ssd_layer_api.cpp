@@ -328,7 +328,7 @@ ssd_status_t norm_fwd(const ssd_norm_shape_t *s, ssd_dtype_t io, const void *x, 
         acc.ok = acc.ok && aligned(y, n);
     else
         acc.in(y, dense);
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_norm_fwd(io == SSD_BF16, acc.ok, a, (hipStream_t)stream);
     return launched(what);
 }
@@ -369,7 +369,7 @@ ssd_status_t ssd_glr_fwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     a.ws_h = bytes ? (float *)((char *)workspace + bytes / 2) : nullptr;
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(y, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_glr_fwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_fwd");
 }
@@ -423,7 +423,7 @@ ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(dy, a.dys)
                           .in(dx, dense).in(dg, dense).in(dz, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_glr_bwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_bwd");
 }
@@ -444,7 +444,7 @@ ssd_status_t ssd_glr_step(const ssd_glr_shape_t *shape, ssd_dtype_t io, const vo
     const ssd::GlrStepArgs a = {x, g, z, s.xs, s.gs, s.zs, A, bias, state, y, s.batch, s.channels, s.normalize};
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(y, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_glr_step(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_step");
 }
@@ -467,7 +467,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(init_states, dense).in(y, dense)
                           .in(final_states, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_conv_fwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_conv_fwd");
 }
@@ -510,7 +510,7 @@ ssd_status_t ssd_conv_bwd(const ssd_conv_shape_t *shape, ssd_dtype_t io, const v
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(dy, a.dys).in(init_states, dense)
                           .in(dx, dense).ok;
     const int run = conv_run(shape, ssd::conv_strip(pair), (hipStream_t)stream);
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_conv_bwd(io == SSD_BF16, pair, a, run, dweight, dbias, (hipStream_t)stream);
     return launched("ssd_conv_bwd");
 }
@@ -530,7 +530,7 @@ ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, ssd_dtype_t io, const 
     a.y = y;
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(state, dense).in(y, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_conv_step(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_conv_step");
 }
@@ -578,7 +578,7 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_shape_t *shape, ssd_dtype_t io, const v
     const int64_t dense = shape->columns * (int64_t)e;
     const bool wide = Access(a.width % n == 0, n, io).in(x, a.xs).in(z, a.zs).in(dy, a.dys).in(dresidual, a.drs)
                           .in(dx, dense).in(dz, dense).ok;
-    (void)hipGetLastError();   // not an earlier call\'s
+    (void)hipGetLastError();   // not an earlier call's
     ssd::launch_norm_bwd(io == SSD_BF16, wide, a, dweight, (hipStream_t)stream);
     return launched("ssd_norm_bwd");
 }

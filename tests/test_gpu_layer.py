@@ -70,6 +70,7 @@ GLR_CASES = [
     (1, 4099, 40, "bf16", False, True, 700, True, None),
     (16, 260, 1056, "bf16", True, True, 90, True, None),      # one split, three rounds
     (3, 901, 1001, "f32", False, True, 0, False, None),
+    (4, 140, 4130, "bf16", True, True, 50, True, None),       # 260 strips: on 256 compute units the last 4 in halves
 ]
 
 
@@ -184,6 +185,34 @@ def test_glr_nonfinite_values_stay_in_their_document(L):
     for k in ("dx", "dg", "dz"):
         assert torch.equal(gd[k][ok], g[k][ok]), k
     assert torch.equal(gd["dinit"], g["dinit"])
+
+
+@pytest.mark.parametrize("sign", [1., -1.])
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("L", [13, 130, 1400])
+def test_glr_a_nan_gate_reaches_the_rest_of_its_document(L, packed, sign):
+    """Whatever the sign of the NaN, and with k = 1, where the input's term of the
+    recurrence stays finite: forward every token behind it, backward every
+    token before it, in its document and in no other."""
+    D = 34
+    io, s, grad = glr_inputs((2, L, D, "f32", False, True, 0, False, None), seed=8)
+    s["normalize"] = False
+    lo, hi = (L // 3, 2 * L // 3) if packed else (0, L)
+    if packed:
+        s["seq_idx"] = torch.zeros(2, L, dtype=torch.int32, device=DEV)
+        s["seq_idx"][:, lo:hi] = 1
+    at = (lo + hi) // 2
+    s["g"] = s["g"].clone()
+    s["g"][0, at] = math.copysign(math.nan, sign)
+    y, f = ssd.ssd_glr_fwd(**s)
+    nan = torch.zeros(2, L, dtype=torch.bool, device=DEV)
+    nan[0, at:hi] = True
+    assert torch.equal(torch.isnan(y), nan[..., None].expand_as(y))
+    assert bool(torch.isnan(f[0]).all()) == (not packed) and torch.isfinite(f[1]).all()
+    dx = ssd.ssd_glr_bwd(**s, **grad)["dx"]
+    nan = torch.zeros(2, L, dtype=torch.bool, device=DEV)
+    nan[0, lo:at] = True
+    assert torch.equal(torch.isnan(dx), nan[..., None].expand_as(dx))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
