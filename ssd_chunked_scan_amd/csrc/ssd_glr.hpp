@@ -88,11 +88,12 @@ struct GlrUnit {
     int ct, blk, b;
 };
 
-template <typename TL>
+template <typename TL, bool REVERSED = false>
 __device__ inline GlrUnit glr_unit(const GlrArgs &a, int nblk) {
     // neighbouring strips share 128-byte lines: keep them on one XCD's L2
     const int nct = (a.channels + TL::CT - 1) / TL::CT;
-    const int u = xcd_contiguous(blockIdx.x, gridDim.x);
+    int u = xcd_contiguous(blockIdx.x, gridDim.x);
+    if (REVERSED) u = (int)gridDim.x - 1 - u;
     GlrUnit r;
     r.ct = u % nct;
     r.blk = (u / nct) % nblk;
@@ -483,10 +484,19 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
 // adjoint it passes on (glr_block_kernel: x, g, dy, z read once, 8 bytes an
 // element in bf16), joined over the row by glr_block_scan_kernel, then this
 // kernel with the same inputs again and the gradients out (14 bytes).  At 8 x
-// 2048 x 5120 with a gate 159 + 13 + 266 us, both passes at 4.2 to 4.4 TB/s
-// and at four fifths of the vector unit.  Taking the rows in groups that stay
-// in the Infinity Cache between the passes was slower (468 us in halves, 521
-// row by row): the launches' ends cost what the second reading gains.
+// 2048 x 5120 with a gate 159 + 13 + 240 us, at four fifths of the vector unit.
+// Taking the rows in groups that stay in the Infinity Cache between the passes
+// was slower (468 us in halves, 521 row by row, for 452 at that time): the
+// launches' ends cost what the second reading gains.  What gains is to take
+// the blocks here in the opposite order, the last ones read first, and to
+// store the gradients without displacing the inputs still cached: 437 us
+// without either, 432 with the order alone, 420 with the stores alone, 410 with
+// both; a convolution, this recurrence and a gated norm with their backward
+// passes 959 -> 943 us, at 2 x 2048 290 -> 289, at 1 x 512 91 -> 89.  Such stores
+// need whole strips that start on 64 bytes (5118 channels: 554 us with them, 477
+// without, 490 before).  The forward passes keep ordinary stores: 151 us for
+// 155 alone, but the next kernel then reads y from memory (2 x 2048, the same
+// three operators: 107 us for 102).
 //
 // One workgroup per (row, block of RT tokens, strip), with the state
 // entering the block from the left (ws_h) and the adjoint from the right
@@ -502,7 +512,7 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
     typedef typename RW::type R;
     __shared__ float2 seg_map[SEG][CT];
     __shared__ float seg_e[SEG][CT], seg_h[SEG][CT];
-    const GlrUnit u = glr_unit<TL>(a, a.nblk);
+    const GlrUnit u = glr_unit<TL, true>(a, a.nblk);
     const int tid = threadIdx.x, cg = tid % TL::CL, seg = tid / TL::CL, m = seg * T;
     const int D = a.channels, L = a.seqlen;
     const int c = u.ct * CT + cg * V;
@@ -631,7 +641,8 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
         const __amdgpu_buffer_rsrc_t og = buffer_of((char *)a.dg + (row + t) * ys);
         const __amdgpu_buffer_rsrc_t oz = buffer_of((char *)a.dz + (row + t) * ys);
         const uint32_t off = (uint32_t)m * (uint32_t)ys + (uint32_t)cb;
-        if (any) {
+        auto grads = [&](auto aux) {
+            constexpr int AUX = decltype(aux)::value;
 #pragma unroll
             for (int i = T - 1; i >= 0; --i) {
                 float dx[V], dg[V], dz[V];
@@ -656,12 +667,16 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
                     }
                 }
                 if (FULL || (cok && ok(i))) {
-                    buffer_store<IO, V>(ox, off, (uint32_t)(i * ys), dx);
-                    buffer_store<IO, V>(og, off, (uint32_t)(i * ys), dg);
-                    if (GATE) buffer_store<IO, V>(oz, off, (uint32_t)(i * ys), dz);
+                    buffer_store<IO, V, AUX>(ox, off, (uint32_t)(i * ys), dx);
+                    buffer_store<IO, V, AUX>(og, off, (uint32_t)(i * ys), dg);
+                    if (GATE) buffer_store<IO, V, AUX>(oz, off, (uint32_t)(i * ys), dz);
                 }
             }
-        }
+        };
+        if (FULL && V == 2 && a.once)
+            grads(std::integral_constant<int, V == 2 ? kOnce : kKeep>{});
+        else if (any)
+            grads(std::integral_constant<int, kKeep>{});
     };
     if ((u.ct + 1) * CT <= D && t + TL::RT <= L)
         block(std::true_type{});

@@ -35,6 +35,7 @@ struct GlrArgs {
     int normalize;
     int cus;                        // forward: compute units
     int whole;                      // forward: units that run as one workgroup, the others as two
+    int once;                       // backward: whether the gradients are stored as kOnce
 };
 
 struct GlrStepArgs {
@@ -140,16 +141,20 @@ __device__ inline R buffer_load(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_
     else return __builtin_amdgcn_raw_buffer_load_b128(b, lane, token, 0);
 }
 
-template <typename IO, int V>
+// A store's cache policy: kOnce marks data that should not push other lines out
+// of the caches (non-temporal).
+enum : int { kKeep = 0, kOnce = 2 };
+
+template <typename IO, int V, int AUX = kKeep>
 __device__ inline void buffer_store(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t token, const float (&f)[V]) {
     typedef typename Words<sizeof(IO) * V>::type R;
     typedef float fv __attribute__((ext_vector_type(V)));
     typedef IO iv __attribute__((ext_vector_type(V)));
     const R r = __builtin_bit_cast(R, __builtin_convertvector(__builtin_bit_cast(fv, f), iv));
-    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(r, b, lane, token, 0);
-    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(r, b, lane, token, 0);
-    else if constexpr (sizeof(R) == 8) __builtin_amdgcn_raw_buffer_store_b64(r, b, lane, token, 0);
-    else __builtin_amdgcn_raw_buffer_store_b128(r, b, lane, token, 0);
+    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(r, b, lane, token, AUX);
+    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(r, b, lane, token, AUX);
+    else if constexpr (sizeof(R) == 8) __builtin_amdgcn_raw_buffer_store_b64(r, b, lane, token, AUX);
+    else __builtin_amdgcn_raw_buffer_store_b128(r, b, lane, token, AUX);
 }
 
 // ------------------------------------------------------------------- maps

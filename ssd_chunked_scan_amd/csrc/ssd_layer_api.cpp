@@ -423,6 +423,7 @@ ssd_status_t ssd_glr_bwd(const ssd_glr_shape_t *shape, ssd_dtype_t io, const voi
     const int64_t dense = shape->channels * (int64_t)e;
     const bool pair = Access(shape->channels % 2 == 0, 2, io).in(x, a.xs).in(g, a.gs).in(z, a.zs).in(dy, a.dys)
                           .in(dx, dense).in(dg, dense).in(dz, dense).ok;
+    a.once = dense % 64 == 0 && aligned(dx, 64) && aligned(dg, 64) && aligned(dz, 64);
     (void)hipGetLastError();   // not an earlier call's
     ssd::launch_glr_bwd(io == SSD_BF16, pair, a, (hipStream_t)stream);
     return launched("ssd_glr_bwd");

@@ -187,6 +187,28 @@ def test_glr_nonfinite_values_stay_in_their_document(L):
     assert torch.equal(gd["dinit"], g["dinit"])
 
 
+@pytest.mark.parametrize("L", [3, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_glr_bwd_outputs_at_any_address(dtype, L):
+    """The gradients do not depend on where the outputs lie (from 64-byte
+    boundaries to those of one element), and nothing beside them is written."""
+    D = 160
+    io, s, grad = glr_inputs((2, L, D, dtype, True, True, 40, True, None), seed=9)
+    want = ssd.ssd_glr_bwd(**s, **grad)
+    exact = glr_reference(s).backward(cpu(grad["dy"]), cpu(grad["dfinal"]))
+    for shift in (0, 1, 2, 64 // torch.tensor([], dtype=io).element_size()):
+        bufs = {k: torch.full((2 * L * D + 256,), 7., dtype=io, device=DEV) for k in ("dx", "dg", "dz")}
+        out = {k: b[64 + shift:64 + shift + 2 * L * D].view(2, L, D) for k, b in bufs.items()}
+        out.update({k: torch.empty_like(want[k]) for k in ("dA", "dbias", "dinit")})
+        got = ssd.ssd_glr_bwd(**s, **grad, out=out)
+        for k in ("dx", "dg", "dz"):
+            within(k, got[k], exact[k], io)
+            if shift != 1:   # single channels a lane: sums in another order
+                assert torch.equal(got[k], want[k]), (k, shift)
+            edge = torch.cat([bufs[k][:64 + shift], bufs[k][64 + shift + 2 * L * D:]])
+            assert (edge == 7).all(), (k, shift)
+
+
 @pytest.mark.parametrize("sign", [1., -1.])
 @pytest.mark.parametrize("packed", [True, False])
 @pytest.mark.parametrize("L", [13, 130, 1400])
