@@ -573,6 +573,9 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
                 }
         }
         auto p_of = [&](int i, int v) { return glr_mark<PACKED>(al[i][v], (cut >> i) & 1); };
+        // (a select: past the row's end x repeats the last token's, and 0 times an
+        // infinity or a NaN would not be 0)
+        auto q_of = [&](int i, int v) { return ok(i) ? k[i][v] * RW::at(xr[i], v) : 0.f; };
         auto e_of = [&](int i, int v) {
             const float d = RW::at(dr[i], v);
             const float e = GATE ? d * (RW::at(zr[i], v) * sz[i][v]) : d;
@@ -584,7 +587,7 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 const float p = p_of(i, v);
-                qs = glr_apply<PACKED>(p, qs, k[i][v] * RW::at(xr[i], v));
+                qs = glr_apply<PACKED>(p, qs, q_of(i, v));
                 ps = glr_join<PACKED>(ps, p);
                 es = glr_apply<PACKED>(ps, e_of(i, v), es);
             }
@@ -632,7 +635,7 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
             float hv = hin[v];
 #pragma unroll
             for (int i = 0; i < T; ++i) {
-                hv = glr_apply<PACKED>(p_of(i, v), hv, k[i][v] * RW::at(xr[i], v));
+                hv = glr_apply<PACKED>(p_of(i, v), hv, q_of(i, v));
                 h[i][v] = hv;
             }
             dA[v] = dbias[v] = 0.f;
@@ -658,6 +661,8 @@ __global__ __launch_bounds__(TL::W * 64, TL::V == 2 && !(sizeof(IO) == 4 && PACK
                         const float rk = k[i][v] > 0.f ? __builtin_amdgcn_rcpf(k[i][v]) : 0.f;
                         dla = fmaf(-G * x, al[i][v] * al[i][v] * rk, dla);
                     }
+                    // (dfinal times a last state that is not finite is no token's)
+                    dla = ok(i) ? dla : 0.f;
                     dg[v] = A[v] * dla * sg[i][v];
                     dA[v] = fmaf(sp[i][v], dla, dA[v]);
                     dbias[v] += dg[v];
