@@ -533,15 +533,5 @@ def ssd_bwd(x, dt, A, B, C, D, dy, seq_idx=None, init_states=None, dfinal=None, 
     return out
 
 
-_LAYER = ("ssd_glr_fwd", "ssd_glr_bwd", "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step",
-          "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd", "GlrShape", "ConvShape", "NormShape")
-
-
-def __getattr__(name):
-    # the layer operators' module imports torch, which this one leaves to its
-    # calls
-    if name in _LAYER:
-        from . import layer
-        value = globals()[name] = getattr(layer, name)
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+from .layer import (ssd_glr_fwd, ssd_glr_bwd, ssd_glr_step, ssd_conv_fwd, ssd_conv_bwd, ssd_conv_step,  # noqa: E402
+                    ssd_norm_fwd, ssd_norm_quant_fwd, ssd_norm_bwd, GlrShape, ConvShape, NormShape)

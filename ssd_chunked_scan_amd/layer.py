@@ -15,9 +15,9 @@ import contextlib
 import ctypes
 from typing import Optional, Tuple
 
-import torch
-
 import ssd_chunked_scan_amd as ssd
+
+torch = None   # from the first call on (_library): the package and the C interface do without it
 
 _I64, _VP = ctypes.c_int64, ctypes.c_void_p
 
@@ -116,8 +116,18 @@ def _ptr(t):
 
 # The current stream's handle of a device, without the Stream object around it
 # (2 us of a 10 us call) where torch offers that.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_stream = None
+
+
+def _library():
+    """libssd.so, and torch with the first call."""
+    global torch, _raw_stream
+    if torch is None:
+        import torch as module
+        _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: module.cuda.current_stream(index).cuda_stream)
+        torch = module
+    return ssd.load_library()
 
 
 class _On:
@@ -222,7 +232,7 @@ def ssd_glr_fwd(x, g, A, bias=None, z=None, seq_idx=None, init_states=None, norm
     fp32 state [b, D] after the last token (None without
     ``return_final_states``).  g, z as x; A (<= 0), bias [D], init_states
     [b, D]: fp32."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _glr_common("ssd_glr_fwd", x, g, A, bias, z, seq_idx, init_states, normalize)
     dev, b, D = x.device, shape.batch, shape.channels
     with _On(dev, stream) as st:
@@ -245,7 +255,7 @@ def ssd_glr_bwd(x, g, A, bias, dy, z=None, seq_idx=None, init_states=None, dfina
     dx, dg, dz (x's dtype), dA, dbias [D] and dinit [b, D] (fp32); dz, dbias and
     dinit are None without z, bias and init_states.  dy as x; dfinal [b, D]
     fp32 or None.  ``out``: the outputs to write, every one that is returned."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _glr_common("ssd_glr_bwd", x, g, A, bias, z, seq_idx, init_states, normalize)
     dev, b, D, f32 = x.device, shape.batch, shape.channels, torch.float32
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)
@@ -265,7 +275,7 @@ def ssd_glr_bwd(x, g, A, bias, dy, z=None, seq_idx=None, init_states=None, dfina
 def ssd_glr_step(x, g, A, state, bias=None, z=None, normalize: bool = True, y=None, stream=None) -> torch.Tensor:
     """One token of ssd_glr_fwd: x, g, z [b, D]; state [b, D] fp32 updated in
     place.  Returns y [b, D]."""
-    lib = ssd.load_library()
+    lib = _library()
     io = _io(x, "ssd_glr_step")
     if x.dim() != 2:
         raise ValueError(f"ssd_glr_step: x must be [b, D], got {tuple(x.shape)}")
@@ -311,7 +321,7 @@ def ssd_conv_fwd(x, weight, bias=None, seq_idx=None, init_states=None, silu: boo
     one before it.  init_states [b, W-1, D] (x's dtype) are the inputs before
     the row.  Returns (y, final_states): the window [b, W-1, D] the next token
     sees (None without ``return_final_states``)."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _conv_common("ssd_conv_fwd", x, weight, bias, seq_idx, init_states, silu)
     dev = x.device
     with _On(dev, stream) as st:
@@ -331,7 +341,7 @@ def ssd_conv_bwd(x, weight, bias, dy, seq_idx=None, init_states=None, dfinal=Non
     of dx (x's dtype), dweight [D, W], dbias [D] (None without bias) and dinit
     [b, W-1, D] (None without init_states), fp32.  dy as x; dfinal [b, W-1, D]
     fp32 or None.  ``out``: the outputs to write, every one that is returned."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _conv_common("ssd_conv_bwd", x, weight, bias, seq_idx, init_states, silu)
     dev, f32 = x.device, torch.float32
     b, D, W = shape.batch, shape.channels, shape.width
@@ -351,7 +361,7 @@ def ssd_conv_bwd(x, weight, bias, dy, seq_idx=None, init_states=None, dfinal=Non
 def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream=None) -> torch.Tensor:
     """One token of ssd_conv_fwd: x [b, D]; state [b, W-1, D] (x's dtype), the
     last W-1 inputs, shifted in place.  Returns y [b, D]."""
-    lib = ssd.load_library()
+    lib = _library()
     io = _io(x, "ssd_conv_step")
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError(f"ssd_conv_step: x must be [b, D] and weight [D, W], got {tuple(x.shape)}, {tuple(weight.shape)}")
@@ -401,7 +411,7 @@ def ssd_norm_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5, ngrou
     groups, times weight [D] (fp32, None: 1): of x, of x + residual (rounded to
     x's dtype, the residual stream), or of x silu(z).  Returns (y, the residual
     stream or None).  ``residual_out`` may be ``residual`` itself."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _norm_fwd("ssd_norm_fwd", x, weight, residual, z, eps, ngroups, residual_out)
     with _On(x.device, stream) as st:
         y = _like(y, "y", x)
@@ -420,7 +430,7 @@ def ssd_norm_quant_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5,
     or None) with y = q * scale, q [..., D] float8_e4m3fn and one fp32 scale =
     max|y| / 448 for each ``block`` = 128 columns of a norm group, or for each
     norm group with ``block`` = 0: scales [..., ngroups * blocks]."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _norm_fwd("ssd_norm_quant_fwd", x, weight, residual, z, eps, ngroups, residual_out)
     shape.quant_block = block
     per = shape.columns // ngroups if ngroups > 0 else 0
@@ -447,7 +457,7 @@ def ssd_norm_bwd(x, weight, dy, z=None, dresidual=None, eps: float = 1e-5, ngrou
     dresidual, the stream's gradient from its other uses, is added to dx, which
     is the gradient of x and of the residual alike.  ``out``: the outputs to
     write, every one that is returned."""
-    lib = ssd.load_library()
+    lib = _library()
     io, shape = _norm_common("ssd_norm_bwd", x, weight, z, eps, ngroups)
     dev = x.device
     shape.dy_stride = _tokens(dy, "dy", x.shape, x.dtype, dev)

@@ -1,0 +1,43 @@
+"""The layer operators' binding on the host: the library without torch, and the
+numbers that its argument structures cannot hold.  CPU only: no kernel is started."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+WITHOUT_TORCH = """
+import ctypes, sys
+if {blocked}:
+    sys.modules["torch"] = None          # any import of it raises ImportError
+import ssd_chunked_scan_amd as ssd
+from ssd_chunked_scan_amd import *       # names only: nothing is called
+lib = ssd.load_library()
+for name in ssd.EXPORTS:
+    assert getattr(lib, name)
+shape = ssd.GlrShape(1, 4096, 64, 0, 0, 0, 0, 1)
+assert lib.ssd_glr_bwd_workspace_bytes(ctypes.byref(shape), 1) == 20 * 64 * 64
+assert lib.ssd_glr_step(None, 1, *[None] * 7, None) == 1 and b"shape" in lib.ssd_last_error()
+assert ssd.ssd_conv_step is ssd_conv_step and ssd.NormShape and ssd.ConvShape
+if {blocked}:
+    try:
+        ssd.ssd_norm_fwd(None)
+    except ImportError:
+        pass
+    else:
+        raise AssertionError("a call without torch")
+else:
+    assert "torch" not in sys.modules
+"""
+
+
+@pytest.mark.parametrize("blocked", [True, False])
+def test_the_library_loads_without_torch(blocked):
+    """The C interface needs no torch: neither the package, its names nor the
+    loaded library import it."""
+    env = dict(os.environ, PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH.format(blocked=blocked)], capture_output=True, text=True,
+                       env=env, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
