@@ -383,7 +383,14 @@ def ssd_conv_step(x, weight, state, bias=None, silu: bool = True, y=None, stream
 # -------------------------------------------------------------------- norm
 
 
+def _fits(name, value, bits):
+    """ctypes drops the bits that a structure's field has no room for."""
+    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+        raise ValueError(f"{name}: {value} does not fit {bits} bits")
+
+
 def _norm_common(name, x, weight, z, eps, ngroups):
+    _fits("ngroups", ngroups, 64)
     io = _io(x, name)
     if x.dim() < 1:
         raise ValueError(f"{name}: x must be [..., D]")
@@ -431,6 +438,7 @@ def ssd_norm_quant_fwd(x, weight=None, residual=None, z=None, eps: float = 1e-5,
     max|y| / 448 for each ``block`` = 128 columns of a norm group, or for each
     norm group with ``block`` = 0: scales [..., ngroups * blocks]."""
     lib = _library()
+    _fits("block", block, 32)
     io, shape = _norm_fwd("ssd_norm_quant_fwd", x, weight, residual, z, eps, ngroups, residual_out)
     shape.quant_block = block
     per = shape.columns // ngroups if ngroups > 0 else 0

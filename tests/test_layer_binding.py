@@ -41,3 +41,25 @@ def test_the_library_loads_without_torch(blocked):
     r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH.format(blocked=blocked)], capture_output=True, text=True,
                        env=env, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("block", [2 ** 32 + 128, 2 ** 32, 128 - 2 ** 32, 2 ** 64 + 128, 2 ** 31])
+def test_a_block_is_not_cut_to_32_bits(block):
+    """The structure's field has 32 bits and ctypes drops the others: 2^32 + 128
+    would be scaled in blocks of 128 into scales allocated for one a row.  (The
+    refusal comes before the one of tensors off the GPU.)"""
+    import torch
+    import ssd_chunked_scan_amd as ssd
+    with pytest.raises(ValueError, match="block"):
+        ssd.ssd_norm_quant_fwd(torch.zeros(2, 256), None, block=block)
+
+
+@pytest.mark.parametrize("ngroups", [2 ** 64 + 2, 2 ** 63, 1 - 2 ** 64])
+def test_ngroups_is_not_cut_to_64_bits(ngroups):
+    import torch
+    import ssd_chunked_scan_amd as ssd
+    x = torch.zeros(2, 256)
+    for call in (lambda: ssd.ssd_norm_fwd(x, None, ngroups=ngroups), lambda: ssd.ssd_norm_bwd(x, None, x, ngroups=ngroups),
+                 lambda: ssd.ssd_norm_quant_fwd(x, None, ngroups=ngroups)):
+        with pytest.raises(ValueError, match="ngroups"):
+            call()
