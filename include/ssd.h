@@ -358,7 +358,11 @@ ssd_status_t ssd_fwd_noalloc(const ssd_shape_t *shape, ssd_dtype_t io,
  * residual_out may be the residual itself and a step's state is updated in
  * place.  Channels and columns are at most 2^20, tokens (batch seqlen, rows)
  * at most 2^30 - 1, strides at most 2^22 elements (2^40 for the norm and for
- * rows of one token). */
+ * rows of one token).  A launch's size bounds them together: the recurrence
+ * takes batch * ceil(seqlen / 64) * ceil(channels / 32) < 2^23 (a step: seqlen
+ * 1) and batch * ceil(channels / 64) < 2^22, the convolution
+ * batch * ceil(seqlen / 64) * ceil(channels / 64) < 2^24; more is
+ * SSD_ERR_UNSUPPORTED. */
 
 /* Gated linear recurrence.  Per channel c, with the same decay map and
  * document resets as ssd_fwd:
@@ -367,7 +371,11 @@ ssd_status_t ssd_fwd_noalloc(const ssd_shape_t *shape, ssd_dtype_t io,
  *   y_t = h_t, or h_t silu(z_t) when z is given
  * r_t = 0 where seq_idx changes between tokens t-1 and t, else 1; the state
  * before token 0 is init_states (0 when NULL); final_states is the state
- * after the row's last token.  States in fp32, all arithmetic in fp32. */
+ * after the row's last token.  States in fp32, all arithmetic in fp32.
+ * With normalize and a constant decay the state has the variance of an
+ * uncorrelated input.  Without it and with A_c = -1 the decay is
+ * 1 - sigmoid(g_t + bias_c), an update gate's, and x_t brings the input's
+ * factor along. */
 typedef struct {
     int64_t batch, seqlen, channels;
     int64_t x_stride, g_stride, z_stride, dy_stride; /* tokens; 0 = dense */
@@ -455,7 +463,7 @@ ssd_status_t ssd_conv_step(const ssd_conv_shape_t *shape, ssd_dtype_t io,
  *       x + residual rounded to the io dtype (written to residual_out)
  *   y = v rsqrt(mean(v^2 over the group) + eps) weight
  * residual and z exclude each other.  Statistics in fp32.  A group has at most
- * 16384 columns. */
+ * 16384 columns; ngroups is at most 65535. */
 typedef struct {
     int64_t rows, columns, ngroups;
     int64_t x_stride, z_stride, residual_stride, dy_stride, dresidual_stride; /* rows; 0 = dense */

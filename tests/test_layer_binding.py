@@ -63,3 +63,27 @@ def test_ngroups_is_not_cut_to_64_bits(ngroups):
                  lambda: ssd.ssd_norm_quant_fwd(x, None, ngroups=ngroups)):
         with pytest.raises(ValueError, match="ngroups"):
             call()
+
+
+def test_the_sizes_at_the_documented_limits():
+    """The largest sizes that include/ssd.h names get past the checks of the shape
+    (to the NULL x), the next ones do not."""
+    import ctypes
+    import ssd_chunked_scan_amd as ssd
+    lib = ssd.load_library()
+    NULL, UNSUPPORTED = 1, 3
+
+    def status(name, shape, pointers, workspace=()):
+        return getattr(lib, name)(ctypes.byref(shape), 1, *[None] * pointers, *workspace, None)
+
+    glr = lambda b, L, D: ssd.GlrShape(b, L, D, 0, 0, 0, 0, 1)
+    for b, L, D, want in (((1 << 23) - 1, 1, 32, UNSUPPORTED), ((1 << 22) - 1, 1, 64, NULL), (1 << 22, 1, 64, UNSUPPORTED),
+                          (1, 64 * ((1 << 23) - 1), 32, NULL), (1, 64 << 23, 32, UNSUPPORTED)):
+        assert status("ssd_glr_fwd", glr(b, L, D), 9, (None, 0)) == want, (b, L, D)
+        if L == 1:
+            assert status("ssd_glr_step", glr(b, L, D), 7) == want
+    conv = lambda b, L, D: ssd.ConvShape(b, L, D, 4, 0, 0, 1)
+    for b, L, D, want in (((1 << 24) - 1, 64, 64, NULL), (1 << 24, 1, 64, UNSUPPORTED), (1, 64, 1 << 20, NULL)):
+        assert status("ssd_conv_fwd", conv(b, L, D), 7) == want, (b, L, D)
+    norm = lambda groups: ssd.NormShape(3, 4 * groups, groups, 0, 0, 0, 0, 0, 1e-5, 0)
+    assert status("ssd_norm_fwd", norm(65535), 6) == NULL and status("ssd_norm_fwd", norm(65536), 6) == UNSUPPORTED
