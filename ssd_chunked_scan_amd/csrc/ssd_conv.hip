@@ -72,10 +72,10 @@ __device__ inline ConvUnit conv_unit(uint32_t u, int nstrip, int nchunk) {
 }
 
 // Consecutive workgroups on one XCD, so that the W - 1 tokens before a chunk
-// come from L2; the rows' offsets in scalar registers.  Two channels a lane:
-// 79 us for 8 x 2048 x 5376 in bf16 (4.5 TB/s); four 86 us, eight 98 us, whose
-// registers leave half and a third of the waves, and 24 tokens instead of 16
-// 78 us.
+// come from L2; the rows' offsets in scalar registers.  74 us for 8 x 2048 x
+// 5376 in bf16 (4.8 TB/s).  Two channels a lane were chosen when that took 79
+// us: four took 86 and eight 98, whose registers leave half and a third of the
+// waves, and 24 tokens instead of 16 took 78.
 template <typename IO, int V, int W, bool PACKED, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     constexpr int T = kConvTokens;

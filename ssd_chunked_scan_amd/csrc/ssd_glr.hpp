@@ -484,13 +484,14 @@ __global__ __launch_bounds__(TL::W * 64) void glr_block_kernel(GlrArgs a, int nb
 // adjoint it passes on (glr_block_kernel: x, g, dy, z read once, 8 bytes an
 // element in bf16), joined over the row by glr_block_scan_kernel, then this
 // kernel with the same inputs again and the gradients out (14 bytes).  At 8 x
-// 2048 x 5120 with a gate 159 + 13 + 240 us, at four fifths of the vector unit.
+// 2048 x 5120 with a gate 408 us (136 + 13 + 271 by the profiler), at four
+// fifths of the vector unit.
 // Taking the rows in groups that stay in the Infinity Cache between the passes
 // was slower (468 us in halves, 521 row by row, for 452 at that time): the
 // launches' ends cost what the second reading gains.  What gains is to take
 // the blocks here in the opposite order, the last ones read first, and to
 // store the gradients without displacing the inputs still cached: 437 us
-// without either, 432 with the order alone, 420 with the stores alone, 410 with
+// without either, 432 with the order alone, 420 with the stores alone, 408 with
 // both; a convolution, this recurrence and a gated norm with their backward
 // passes 959 -> 943 us, at 2 x 2048 290 -> 289, at 1 x 512 91 -> 89.  Such stores
 // need whole strips that start on 64 bytes (5118 channels: 554 us with them, 477

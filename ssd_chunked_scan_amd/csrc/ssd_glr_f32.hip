@@ -8,8 +8,8 @@ namespace ssd {
 SSD_GLR_INSTANTIATE(float)
 
 // Joins the blocks of a row, 64 channels per workgroup: 16 threads per channel
-// take a run of blocks each, so that a long row (65536 tokens: 512 blocks) is
-// 32 dependent steps twice and not 512.  ws_h becomes the state entering each
+// take a run of blocks each, so that a long row (65536 tokens: 1024 blocks of
+// the backward pass) is 64 dependent steps twice and not 1024.  ws_h becomes the state entering each
 // block, ws_e the adjoint entering it from behind; the adjoint leaving the
 // first block is the gradient of init.
 template <bool PACKED>

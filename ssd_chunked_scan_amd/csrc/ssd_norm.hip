@@ -276,6 +276,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormArgs a)
 // so that two workgroups of ten waves fit a compute unit at 5120 columns
 // (195 us for 16384 gated rows, 4.3 TB/s; 16 columns a thread in half the
 // threads spills: 403 us; loading a row ahead costs one of the two: 199 us).
+// Odd groups of over 8192 columns have no other way than 16 single columns a
+// thread, here up to 236 bytes of scratch a thread and forward 224: 16384 fp32
+// rows of 8195 with the residual take 880 us, floor 438.
 template <typename IO, int V, bool WAVE, int K, bool GATE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 5 : 4) void norm_bwd_kernel(NormArgs a) {
     constexpr int RPB = WAVE ? 4 : 1;
