@@ -279,7 +279,7 @@ def _plain_block_bwd(s):
     h = ds * scale * gate * s["post"]
     m = (ds * gate * n1).sum(0)
     return dict(dx=(r1 * (h - n1 * (h * n1).mean(-1, keepdim=True))).to(io), dresidual=(s["alpha"] * ds).to(io), dz=dz,
-                dpost=m * scale, dpre=(dy * n2).sum(0), dscale=None if s["scale"] is None else m * s["post"])
+                dpost_weight=m * scale, dpre_weight=(dy * n2).sum(0), dscale=None if s["scale"] is None else m * s["post"])
 
 
 _PLAIN = dict(mx4_quant=_plain_mx4_quant, mx4_linear=_plain_mx4_linear, mx4_matmul=_plain_mx4_matmul,
@@ -404,7 +404,7 @@ def _exact_block(s):
     up = ds * silu * scale * post
     dx = (up - n1 * ((up * n1).sum(-1, keepdim=True) / c)) / rms1
     return dict(dx=dx, dresidual=s["alpha"] * ds, dz=None if z is None else ds * scale * post * n1 * slope,
-                dpost=(ds * scale * silu * n1).sum(0), dpre=(dy * n2).sum(0),
+                dpost_weight=(ds * scale * silu * n1).sum(0), dpre_weight=(dy * n2).sum(0),
                 dscale=None if s["scale"] is None else (ds * post * silu * n1).sum(0))
 
 
