@@ -504,6 +504,115 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_shape_t *shape, ssd_dtype_t io,
                           const void *dresidual, void *dx, void *dz, float *dweight,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Operators between the layers --------------------------------------
+ *
+ * What stands between two blocks of a residual stream: the norm after one block
+ * and the norm before the next as one operator, with 8-bit checkpoints for its
+ * backward pass, and the projections in 4 bits.  Conventions as for the layer
+ * operators above: strides, ownership, threading, graphs, fixed order of sums. */
+
+/* Block norm.  For each row of columns <= 16384, in fp32 but for the stream:
+ *   n1 = x / sqrt(mean(x^2) + eps)                  the norm after the block
+ *   b  = scale post_weight n1 silu(z)               its gate and residual scale
+ *   s  = alpha residual + b, rounded to the io dtype (written to residual_out)
+ *   y  = s / sqrt(mean(s^2) + eps) pre_weight       the norm before the next
+ * z (NULL: no gate), post_weight, pre_weight and scale ([columns] fp32,
+ * NULL: 1) are optional; alpha is 1 for a plain residual stream. */
+typedef struct {
+    int64_t rows, columns;
+    int64_t x_stride, z_stride, residual_stride, dy_stride, dresidual_stride; /* rows; 0 = dense */
+    float eps;            /* > 0, finite    */
+    float alpha;          /* finite         */
+    int64_t reserved[4];  /* must be zero   */
+} ssd_block_shape_t;
+
+/* 8-bit copies of what the backward pass reads: x, z (both pointers NULL
+ * without a gate) and the stream residual_out, each e4m3 [rows][columns] with
+ * fp32 scales [rows][ceil(columns / 128)], in the format of
+ * ssd_norm_quant_fwd with quant_block 128.  A block of 128 with an infinity or a
+ * NaN stands for NaN. */
+typedef struct {
+    void *x;
+    float *x_scales;
+    void *z;
+    float *z_scales;
+    void *residual;
+    float *residual_scales;
+} ssd_block_checkpoint_t;
+
+/* x, residual, z, y, residual_out: io dtype; residual_out may be the residual
+ * itself.  checkpoint (nullable): where to write the copies.  No workspace. */
+ssd_status_t ssd_block_norm_fwd(const ssd_block_shape_t *shape, ssd_dtype_t io,
+                                const void *x, const void *residual,
+                                const float *post_weight, const float *pre_weight,
+                                const void *z, const float *scale,
+                                void *y, void *residual_out,
+                                const ssd_block_checkpoint_t *checkpoint, void *stream);
+
+/* Backward, from dy and dresidual_out (nullable: the gradient of residual_out
+ * from its other uses; its stride is dresidual_stride).  x, z and residual_out (its
+ * stride is residual_stride) as the forward call saw and left them, or NULL
+ * with a checkpoint, which stands for all three: the gradients are then those
+ * at the values that the checkpoint holds.  dx, dresidual, dz (exactly with a
+ * gate): io dtype, dense; dpost_weight, dpre_weight, dscale [columns] fp32,
+ * each exactly when the forward argument is given.  Workspace:
+ * ssd_block_norm_bwd_workspace_bytes (none needed without those three),
+ * 16-byte aligned, queried with the device that will run the call current. */
+size_t ssd_block_norm_bwd_workspace_bytes(const ssd_block_shape_t *shape, ssd_dtype_t io);
+ssd_status_t ssd_block_norm_bwd(const ssd_block_shape_t *shape, ssd_dtype_t io,
+                                const void *x, const void *residual_out,
+                                const float *post_weight, const float *pre_weight,
+                                const void *z, const float *scale,
+                                const void *dy, const void *dresidual_out,
+                                const ssd_block_checkpoint_t *checkpoint,
+                                void *dx, void *dresidual, void *dz,
+                                float *dpost_weight, float *dpre_weight, float *dscale,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Microscaled 4-bit floating point (OCP MX, MXFP4).  A row's columns are cut
+ * into blocks of 32.  With m = max |x| of a block its scale is 2^(byte - 127),
+ * byte = max(floor(log2 m) + 125, 0) (0 for m = 0), and each value is the
+ * e2m1 number (0, 1/2, 1, 3/2, 2, 3, 4, 6 with a sign) nearest to x / scale,
+ * ties to the even code, above 6: 6.  A block with an infinity or a NaN gets byte 255
+ * and codes 0, and stands for NaN.
+ * Layout: columns are padded with zeros to kp = 128 ceil(columns / 128); q is
+ * [rows][kp / 2] bytes, the earlier column in the low half, 16-byte aligned;
+ * scales is [kp / 128][rows][4] bytes, 4-byte aligned: the four blocks of 128
+ * columns together, the rows next to each other. */
+typedef struct {
+    int64_t rows, columns;
+    int64_t outputs;      /* of a product; 0 for quant and dequant       */
+    int64_t x_stride;     /* rows of x; 0 = dense, and without an x      */
+    int64_t reserved[4];  /* must be zero                                */
+} ssd_mx4_shape_t;
+
+/* x: io dtype.  rows / 16 * columns / 512, rounded up, is at most 2^24. */
+ssd_status_t ssd_mx4_quant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const void *x,
+                           void *q, void *scales, void *stream);
+
+/* The values that q and scales stand for, in the io dtype (which holds them
+ * exactly), dense. */
+ssd_status_t ssd_mx4_dequant(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
+                             const void *q, const void *scales, void *y, void *stream);
+
+/* y[r][n] = sum_c a[r][c] w[n][c] + bias[n]: a from q and scales [rows], w from
+ * wq and wscales [outputs], both of `columns` columns; products of codes exact,
+ * sums in fp32, y [rows][outputs] in the io dtype, dense; bias [outputs]
+ * fp32, nullable.  rows / 64 * outputs / 64, rounded up, is at most 2^24.
+ * No workspace. */
+ssd_status_t ssd_mx4_matmul(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
+                            const void *q, const void *scales,
+                            const void *wq, const void *wscales, const float *bias,
+                            void *y, void *stream);
+
+/* The same with a quantised from x [rows][columns] (io dtype) on the way, as
+ * ssd_mx4_quant does.  Workspace: ssd_mx4_linear_workspace_bytes (0 for up to
+ * 16 rows), 16-byte aligned. */
+size_t ssd_mx4_linear_workspace_bytes(const ssd_mx4_shape_t *shape, ssd_dtype_t io);
+ssd_status_t ssd_mx4_linear(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const void *x,
+                            const void *wq, const void *wscales, const float *bias,
+                            void *y, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Debug exports (tests only) ---------------------------------------
  *
  * Segsum factor records.  The hierarchy-aware segsum (page "GPU Hierarchy

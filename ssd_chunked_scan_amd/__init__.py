@@ -23,6 +23,8 @@ __all__ = [
     "ssd_decode_step",
     "ssd_glr_fwd", "ssd_glr_bwd", "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd", "ssd_conv_step",
     "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd",
+    "ssd_block_norm_fwd", "ssd_block_norm_bwd",
+    "ssd_mx4_quant", "ssd_mx4_dequant", "ssd_mx4_matmul", "ssd_mx4_linear",
     "SsdError", "library_path", "load_library", "STATUS", "EXPORTS",
 ]
 
@@ -43,6 +45,9 @@ EXPORTS = ["ssd_fwd_workspace_bytes", "ssd_fwd", "ssd_fwd_ex_workspace_bytes", "
            "ssd_glr_step", "ssd_conv_fwd", "ssd_conv_bwd_workspace_bytes", "ssd_conv_bwd",
            "ssd_conv_step", "ssd_norm_fwd", "ssd_norm_quant_fwd", "ssd_norm_bwd_workspace_bytes",
            "ssd_norm_bwd",
+           "ssd_block_norm_fwd", "ssd_block_norm_bwd_workspace_bytes", "ssd_block_norm_bwd",
+           "ssd_mx4_quant", "ssd_mx4_dequant", "ssd_mx4_matmul", "ssd_mx4_linear_workspace_bytes",
+           "ssd_mx4_linear",
            "ssd_status_str", "ssd_last_error", "ssd_version"]
 # segsum evaluations of the mask export (ssd.h SSD_SEGSUM_*)
 SEGSUM = {"hierarchy": 0, "direct": 1, "diff": 2}
@@ -133,8 +138,9 @@ def load_library():
     lib.ssd_debug_exp2_probe.restype = i32
     lib.ssd_fwd_noalloc.argtypes = fwd_args[:13] + [vp]
     lib.ssd_fwd_noalloc.restype = i32
-    from . import layer
+    from . import block, layer
     layer.declare(lib)
+    block.declare(lib)
     lib.ssd_status_str.argtypes = [i32]
     lib.ssd_status_str.restype = ctypes.c_char_p
     lib.ssd_last_error.argtypes = []
@@ -535,3 +541,5 @@ def ssd_bwd(x, dt, A, B, C, D, dy, seq_idx=None, init_states=None, dfinal=None, 
 
 from .layer import (ssd_glr_fwd, ssd_glr_bwd, ssd_glr_step, ssd_conv_fwd, ssd_conv_bwd, ssd_conv_step,  # noqa: E402
                     ssd_norm_fwd, ssd_norm_quant_fwd, ssd_norm_bwd, GlrShape, ConvShape, NormShape)
+from .block import (ssd_block_norm_fwd, ssd_block_norm_bwd, ssd_mx4_quant, ssd_mx4_dequant,  # noqa: E402
+                    ssd_mx4_matmul, ssd_mx4_linear, BlockShape, BlockCheckpoint, Mx4Shape)

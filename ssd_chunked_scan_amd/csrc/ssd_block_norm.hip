@@ -1,0 +1,495 @@
+// The seam between two blocks of a residual stream (ssd.h, ssd_block_norm_*):
+//
+//   n1 = x rstd1      b = scale post n1 silu(z)      s = alpha residual + b
+//   n2 = s rstd2      y = n2 pre                     rstd = 1 / sqrt(mean(.^2) + eps)
+//
+// and its gradient, with c = scale post and dsn the gradient of s from its other
+// uses:
+//
+//   g = pre dy        ds = rstd2 (g - n2 mean(g n2)) + dsn     dresidual = alpha ds
+//   h = ds c silu(z)  dx = rstd1 (h - n1 mean(h n1))           dz = ds c n1 silu'(z)
+//   dpre = sum_rows dy n2     m = sum_rows ds silu(z) n1       dpost = scale m
+//                                                              dscale = post m
+//
+// Memory-bound: each input read once and each output written once, a row held
+// in registers between its sums (the layout of ssd_norm.hpp).  Two sums of a
+// row depend on each other, forward s on x's and backward h on s's; the next row's
+// loads are under way meanwhile.  The gradients of the two factors of c are the
+// same column sum m, so that two sums a column are carried and not three.
+//
+// With checkpoints (CKPT) x, z and s are also written as e4m3 with a scale
+// per 128 columns, and backward reads those instead: 13 bytes a column
+// instead of 16 in bf16, and 3 kept instead of 6.
+#include <algorithm>
+
+#include "ssd_block.hpp"
+#include "ssd_norm.hpp"
+
+namespace ssd {
+
+// Sums of N values over a row's threads, in every one of them.  One barrier: the
+// caller alternates between two places in LDS, so that a place is written again
+// only after a later sum's barrier.
+template <bool WAVE, int N>
+__device__ inline void row_sums(float (&v)[N], float *lds) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (!WAVE) {
+        if (threadIdx.x % 64 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds[threadIdx.x / 64 * N + i] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+        for (int w = 0; w < (int)blockDim.x / 64; ++w) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += lds[w * N + i];
+        }
+    }
+}
+
+// A row's values as e4m3 with a scale per 128 columns: q at the row's start, sc
+// its scales.
+template <int V, int K>
+__device__ inline void store_checkpoint(uint8_t *q, float *sc, const float (&val)[K][V], int tid, int nthr, int npack) {
+    constexpr int PER = V == 1 ? 2 : 1, LANES = V == 1 ? 64 : 128 / V;
+#pragma unroll
+    for (int k = 0; k < K; k += PER) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (pack_at<V>(k + j, tid, nthr) < npack) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) m = max(m, abs_bits(val[k + j][v]));
+            }
+        const float mx = __uint_as_float(max(lanes_max<LANES>(m), kMinMost));
+        const float inv = 448.f / mx;
+        const int p0 = pack_at<V>(k, tid, nthr);
+        if (tid % LANES == 0 && p0 < npack) sc[p0 * V / 128] = mx / 448.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int p = pack_at<V>(k + j, tid, nthr);
+            if (p < npack) store_e4m3<V>(q + p * V, val[k + j], inv);
+        }
+    }
+}
+
+// V values of a checkpoint as they wait in registers.
+template <int V>
+struct Kept {
+    uint32_t w[V == 8 ? 2 : 1];
+    float scale;
+};
+
+template <int V>
+__device__ inline Kept<V> load_kept(const uint8_t *q, const float *sc, int p) {
+    Kept<V> r;
+    if constexpr (V == 8) {
+        const Pack<uint32_t, 2> t = *(const Pack<uint32_t, 2> *)(q + p * V);
+        r.w[0] = t.v[0];
+        r.w[1] = t.v[1];
+    } else if constexpr (V == 4) {
+        r.w[0] = *(const uint32_t *)(q + p * V);
+    } else {
+        r.w[0] = q[p];
+    }
+    r.scale = sc[p * V / 128];
+    return r;
+}
+
+template <int V>
+__device__ inline void kept_values(const Kept<V> &r, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = __builtin_amdgcn_cvt_f32_fp8((int)r.w[0], 0) * r.scale;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], true);
+            f[4 * i] = lo[0] * r.scale;
+            f[4 * i + 1] = lo[1] * r.scale;
+            f[4 * i + 2] = hi[0] * r.scale;
+            f[4 * i + 3] = hi[1] * r.scale;
+        }
+    }
+}
+
+template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs a) {
+    constexpr int RPB = WAVE ? 4 : 1;   // rows a workgroup takes at a time
+    __shared__ float lds[2][16];
+    const int tid = WAVE ? threadIdx.x % 64 : threadIdx.x, nthr = WAVE ? 64 : blockDim.x;
+    const int npack = a.columns / V, nscale = (a.columns + 127) / 128;
+    const float inv_n = 1.f / (float)a.columns;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x / 64 : 0);
+    Pack<IO, V> xr[K], rr[K], zr[K], xn[K], rn[K], zn[K];
+    auto load = [&](int64_t r, Pack<IO, V> (&x)[K], Pack<IO, V> (&s)[K], Pack<IO, V> (&z)[K]) {
+        const char *xb = (const char *)a.x + r * a.xs, *sb = (const char *)a.residual + r * a.rs;
+        const char *zb = (const char *)a.z + r * a.zs;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                const int64_t off = p * (V * (int)sizeof(IO));
+                x[k] = load_pack<IO, V>(xb + off);
+                s[k] = load_pack<IO, V>(sb + off);
+                if (GATE) z[k] = load_pack<IO, V>(zb + off);
+            }
+        }
+    };
+    if (row < a.rows) load(row, xr, rr, zr);
+    constexpr bool HOLD = K * V <= 8;   // the weights stay in registers
+    auto weight1 = [&](int p, int v) {
+        const int c = p * V + v;
+        return (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
+    };
+    auto weight2 = [&](int p, int v) { return a.pre ? a.pre[p * V + v] : 1.f; };
+    float w1[HOLD ? K : 1][HOLD ? V : 1], w2[HOLD ? K : 1][HOLD ? V : 1];
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = min(pack_at<V>(k, tid, nthr), npack - 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                w1[k][v] = weight1(p, v);
+                w2[k][v] = weight2(p, v);
+            }
+        }
+    }
+    for (; row < a.rows; row += step) {
+        if (row + step < a.rows) load(row + step, xn, rn, zn);
+        float val[K][V], sum[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (pack_at<V>(k, tid, nthr) < npack) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    val[k][v] = (float)xr[k].v[v];
+                    sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
+                }
+            }
+        if constexpr (CKPT)
+            store_checkpoint<V, K>(a.xq + row * a.columns, a.xsc + row * nscale, val, tid, nthr, npack);
+        row_sums<WAVE, 1>(sum, lds[0]);
+        const float rstd1 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
+        if constexpr (CKPT && GATE) {
+            float z[K][V];
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) z[k][v] = (float)zr[k].v[v];
+            store_checkpoint<V, K>(a.zq + row * a.columns, a.zsc + row * nscale, z, tid, nthr, npack);
+        }
+        sum[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                Pack<IO, V> st;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float w, b = val[k][v] * rstd1;
+                    if constexpr (HOLD) w = w1[k][v];
+                    else w = weight1(p, v);
+                    b *= w;
+                    if (GATE) {
+                        const float z = (float)zr[k].v[v];
+                        b *= z * sigmoid_f32(z);
+                    }
+                    // the stream is kept in the io type, and the second norm
+                    // is of what it holds, which is what backward reads
+                    st.v[v] = (IO)fmaf(a.alpha, (float)rr[k].v[v], b);
+                    val[k][v] = (float)st.v[v];
+                    sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
+                }
+                *(Pack<IO, V> *)((IO *)a.residual_out + row * a.columns + p * V) = st;
+            }
+        }
+        if constexpr (CKPT)
+            store_checkpoint<V, K>(a.sq + row * a.columns, a.ssc + row * nscale, val, tid, nthr, npack);
+        row_sums<WAVE, 1>(sum, lds[1]);
+        const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float w;
+                    if constexpr (HOLD) w = w2[k][v];
+                    else w = weight2(p, v);
+                    val[k][v] = val[k][v] * rstd2 * w;
+                }
+                store_pack<IO, V>((IO *)a.y + row * a.columns + p * V, val[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            xr[k] = xn[k];
+            rr[k] = rn[k];
+            zr[k] = zn[k];
+        }
+    }
+}
+
+// Backward: a.parts workgroups take the rows in turn and keep their columns'
+// two sums in registers; each leaves a row of parts [2][columns]: m, dpre.
+template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_bwd_kernel(BlockArgs a) {
+    constexpr int RPB = WAVE ? 4 : 1;
+    __shared__ float lds[2][48];
+    __shared__ float red[WAVE ? 4 : 1][WAVE ? 64 * K * V : 1];
+    const int tid = WAVE ? threadIdx.x % 64 : threadIdx.x, nthr = WAVE ? 64 : blockDim.x;
+    const int wave = threadIdx.x / 64;
+    const int npack = a.columns / V, nscale = (a.columns + 127) / 128;
+    const float inv_n = 1.f / (float)a.columns;
+    constexpr bool HOLD = K * V <= 8;
+    auto weight1 = [&](int p, int v) {
+        const int c = p * V + v;
+        return (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
+    };
+    auto weight2 = [&](int p, int v) { return a.pre ? a.pre[p * V + v] : 1.f; };
+    float w1[HOLD ? K : 1][HOLD ? V : 1], w2[HOLD ? K : 1][HOLD ? V : 1], dm[K][V], dp[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int p = min(pack_at<V>(k, tid, nthr), npack - 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (HOLD) {
+                w1[k][v] = weight1(p, v);
+                w2[k][v] = weight2(p, v);
+            }
+            dm[k][v] = dp[k][v] = 0.f;
+        }
+    }
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? wave : 0);
+    Pack<IO, V> yr[K], gr[K], xr[CKPT ? 1 : K], sr[CKPT ? 1 : K], zr[CKPT ? 1 : K];
+    Kept<V> xk[CKPT ? K : 1], sk[CKPT ? K : 1], zk[CKPT ? K : 1];
+    auto load = [&](int64_t r) {
+        const char *yb = (const char *)a.dy + r * a.dys, *gb = (const char *)a.dresidual_out + r * a.drs;
+        const char *xb = (const char *)a.x + r * a.xs, *sb = (const char *)a.residual + r * a.rs;
+        const char *zb = (const char *)a.z + r * a.zs;
+        const int64_t at = r * a.columns, sc = r * nscale;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                const int64_t off = p * (V * (int)sizeof(IO));
+                yr[k] = load_pack<IO, V>(yb + off);
+                if (a.dresidual_out) gr[k] = load_pack<IO, V>(gb + off);
+                if constexpr (CKPT) {
+                    xk[k] = load_kept<V>(a.xq + at, a.xsc + sc, p);
+                    sk[k] = load_kept<V>(a.sq + at, a.ssc + sc, p);
+                    if (GATE) zk[k] = load_kept<V>(a.zq + at, a.zsc + sc, p);
+                } else {
+                    xr[k] = load_pack<IO, V>(xb + off);
+                    sr[k] = load_pack<IO, V>(sb + off);
+                    if (GATE) zr[k] = load_pack<IO, V>(zb + off);
+                }
+            }
+        }
+    };
+    auto value = [&](const auto &raw, const auto &kept, int k, float (&f)[V]) {
+        if constexpr (CKPT) {
+            kept_values<V>(kept[k], f);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = (float)raw[k].v[v];
+        }
+    };
+    if (row < a.rows) load(row);
+    for (; row < a.rows; row += step) {
+        float sums[3] = {0.f, 0.f, 0.f};   // of x^2, s^2, g s
+        float n1[K][V], h[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                float s[V];
+                value(xr, xk, k, n1[k]);
+                value(sr, sk, k, s);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float w;
+                    if constexpr (HOLD) w = w2[k][v];
+                    else w = weight2(p, v);
+                    sums[0] = fmaf(n1[k][v], n1[k][v], sums[0]);
+                    sums[1] = fmaf(s[v], s[v], sums[1]);
+                    sums[2] = fmaf(w * (float)yr[k].v[v], s[v], sums[2]);
+                }
+            }
+        }
+        row_sums<WAVE, 3>(sums, lds[0]);
+        const float rstd1 = 1.f / __builtin_sqrtf(fmaf(sums[0], inv_n, a.eps));
+        const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sums[1], inv_n, a.eps));
+        const float mean2 = sums[2] * rstd2 * inv_n;   // of g n2
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                float s[V], z[V], dr[V], dz[V];
+                value(sr, sk, k, s);
+                if (GATE) value(zr, zk, k, z);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float c, w;
+                    if constexpr (HOLD) {
+                        c = w1[k][v];
+                        w = w2[k][v];
+                    } else {
+                        c = weight1(p, v);
+                        w = weight2(p, v);
+                    }
+                    const float dy = (float)yr[k].v[v], n2 = s[v] * rstd2;
+                    dp[k][v] = fmaf(dy, n2, dp[k][v]);
+                    float ds = rstd2 * fmaf(-n2, mean2, w * dy);
+                    if (a.dresidual_out) ds += (float)gr[k].v[v];
+                    dr[v] = a.alpha * ds;
+                    n1[k][v] *= rstd1;
+                    float t = ds;
+                    if (GATE) {
+                        const float sig = sigmoid_f32(z[v]);
+                        dz[v] = ds * c * n1[k][v] * (sig * fmaf(z[v], 1.f - sig, 1.f));
+                        t = ds * (z[v] * sig);
+                    }
+                    dm[k][v] = fmaf(t, n1[k][v], dm[k][v]);
+                    h[k][v] = t * c;
+                    sum[0] = fmaf(h[k][v], n1[k][v], sum[0]);
+                }
+                const int64_t at = row * a.columns + p * V;
+                store_pack<IO, V>((IO *)a.dresidual + at, dr);
+                if (GATE) store_pack<IO, V>((IO *)a.dz + at, dz);
+            }
+        }
+        if (row + step < a.rows) load(row + step);
+        row_sums<WAVE, 1>(sum, lds[1]);
+        const float mean1 = sum[0] * inv_n;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+                float dx[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) dx[v] = rstd1 * fmaf(-n1[k][v], mean1, h[k][v]);
+                store_pack<IO, V>((IO *)a.dx + row * a.columns + p * V, dx);
+            }
+        }
+    }
+    if (!a.part) return;
+    float *out = a.part + (int64_t)blockIdx.x * 2 * a.columns;
+    if constexpr (WAVE) {
+        auto join = [&](const float (&d)[K][V], float *to) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) red[wave][pack_at<V>(k, tid, nthr) * V + v] = d[k][v];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.columns; c += 256)
+                to[c] = ((red[0][c] + red[1][c]) + red[2][c]) + red[3][c];
+            __syncthreads();
+        };
+        join(dm, out);
+        join(dp, out + a.columns);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = pack_at<V>(k, tid, nthr);
+            if (p < npack) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    out[p * V + v] = dm[k][v];
+                    out[a.columns + p * V + v] = dp[k][v];
+                }
+            }
+        }
+    }
+}
+
+// Sums the parts in a fixed order: 64 columns of one plane a workgroup, 16
+// threads a column over runs of parts, joined in order.
+__global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x % 64, run = threadIdx.x / 64, n = a.columns;
+    const int ncol = (n + 63) / 64, plane = blockIdx.x / ncol, c = blockIdx.x % ncol * 64 + lane;
+    const int per = (a.parts + 15) / 16, k0 = min(run * per, a.parts), k1 = min(k0 + per, a.parts);
+    const float *p = a.part + (int64_t)plane * n + min(c, n - 1);
+    float acc = 0.f;
+#pragma unroll 8
+    for (int k = k0; k < k1; ++k) acc += p[(int64_t)k * 2 * n];
+    s[run][lane] = acc;
+    __syncthreads();
+    if (run == 0 && c < n) {
+        for (int r = 1; r < 16; ++r) acc += s[r][lane];
+        if (plane == 1) {
+            if (a.dpre) a.dpre[c] = acc;
+        } else {
+            if (a.dpost) a.dpost[c] = a.scale ? acc * a.scale[c] : acc;
+            if (a.dscale) a.dscale[c] = a.post ? acc * a.post[c] : acc;
+        }
+    }
+}
+
+template <typename IO, int V, bool WAVE, int K>
+static void block_fwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
+    const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
+    const dim3 grid((unsigned)std::min(rows, std::max<int64_t>(1, (int64_t)a.cus * (2048 / nthr))));
+#define SSD_BLOCK_FWD(G, C)                                                                                  \
+    if (!a.z == !G && !a.xq == !C)                                                                           \
+        hipLaunchKernelGGL((block_fwd_kernel<IO, V, WAVE, K, G, C>), grid, dim3(nthr), 0, stream, a);
+    SSD_BLOCK_FWD(false, false)
+    SSD_BLOCK_FWD(false, true)
+    SSD_BLOCK_FWD(true, false)
+    SSD_BLOCK_FWD(true, true)
+#undef SSD_BLOCK_FWD
+}
+
+template <typename IO, int V, bool WAVE, int K>
+static void block_bwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
+    const dim3 grid((unsigned)a.parts);
+#define SSD_BLOCK_BWD(G, C)                                                                                  \
+    if (!a.dz == !G && !a.xq == !C)                                                                          \
+        hipLaunchKernelGGL((block_bwd_kernel<IO, V, WAVE, K, G, C>), grid, dim3(nthr), 0, stream, a);
+    SSD_BLOCK_BWD(false, false)
+    SSD_BLOCK_BWD(false, true)
+    SSD_BLOCK_BWD(true, false)
+    SSD_BLOCK_BWD(true, true)
+#undef SSD_BLOCK_BWD
+}
+
+// As the norm's kernels: a wave per row where it can hold KW packs a lane, a
+// workgroup of KB packs a thread while 1024 threads can hold the row, else of KX.
+#define SSD_BLOCK_SHAPE(launch)                                        \
+    const int npack = a.columns / V;                                   \
+    if (npack <= 64 * KW)                                              \
+        launch<IO, V, true, KW>(a, stream, 256);                       \
+    else if (npack <= 1024 * KB)                                       \
+        launch<IO, V, false, KB>(a, stream, norm_threads(npack, KB));  \
+    else                                                               \
+        launch<IO, V, false, KX>(a, stream, norm_threads(npack, KX));
+
+template <typename IO, int V, int KW, int KB, int KX>
+static void block_fwd_shape(const BlockArgs &a, hipStream_t stream) { SSD_BLOCK_SHAPE(block_fwd_launch) }
+
+template <typename IO, int V, int KW, int KB, int KX>
+static void block_bwd_shape(const BlockArgs &a, hipStream_t stream) { SSD_BLOCK_SHAPE(block_bwd_launch) }
+
+void launch_block_fwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {
+    if (bf16_io)
+        wide ? block_fwd_shape<bf16, 8, 1, 1, 2>(a, stream) : block_fwd_shape<bf16, 1, 8, 8, 16>(a, stream);
+    else
+        wide ? block_fwd_shape<float, 4, 2, 2, 4>(a, stream) : block_fwd_shape<float, 1, 8, 8, 16>(a, stream);
+}
+
+void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {
+    if (bf16_io)
+        wide ? block_bwd_shape<bf16, 8, 1, 1, 2>(a, stream) : block_bwd_shape<bf16, 1, 4, 4, 16>(a, stream);
+    else
+        wide ? block_bwd_shape<float, 4, 2, 2, 4>(a, stream) : block_bwd_shape<float, 1, 4, 4, 16>(a, stream);
+    if (a.part) hipLaunchKernelGGL(block_finish_kernel, dim3((a.columns + 63) / 64 * 2), dim3(1024), 0, stream, a);
+}
+
+}  // namespace ssd
