@@ -176,6 +176,14 @@ def check_mfma_result_reads(asm_text: str, where: str) -> int:
 
 _VMEM = ("global_load", "global_store", "buffer_load", "buffer_store", "scratch_load",
          "scratch_store", "flat_load", "flat_store", "global_atomic", "buffer_atomic")
+
+
+def _loads_to_lds(text: str) -> bool:
+    """A direct-to-LDS load: by its opcode, or a buffer load with the lds modifier."""
+    return text.startswith(("global_load_lds", "buffer_load_lds")) or \
+        (text.startswith("buffer_load") and text.endswith(" lds"))
+
+
 _WAIT_VM = re.compile(r"s_waitcnt\s+vmcnt\((\d+)\)")
 VMCNT_MAX = 63
 
@@ -228,7 +236,7 @@ def check_counted_barrier_waits(asm_text: str, where: str) -> int:
                         if op.startswith(("s_branch", "s_cbranch", "s_setpc")):
                             raise RuntimeError(f"{where}: {fname}: touch wait '{text}' reaches a "
                                                f"branch before {m.group(1)} vector-memory operations")
-                        if op.startswith(("global_load_lds", "buffer_load_lds")):
+                        if _loads_to_lds(t):
                             q2 = j - 1
                             while q2 >= 0 and items[q2][0] == "ins" and not items[q2][1].startswith(_VMEM):
                                 q2 -= 1
@@ -253,7 +261,7 @@ def check_counted_barrier_waits(asm_text: str, where: str) -> int:
                     if op.startswith(("s_branch", "s_cbranch", "s_setpc")):
                         raise RuntimeError(f"{where}: {fname}: lookahead wait '{text}' reaches a "
                                            f"branch before {m.group(1)} direct-to-LDS loads")
-                    if op.startswith(("global_load_lds", "buffer_load_lds")):
+                    if _loads_to_lds(t):
                         need -= 1
                     elif op.startswith(_VMEM):
                         raise RuntimeError(f"{where}: {fname}: lookahead wait '{text}' would leave "
@@ -266,7 +274,7 @@ def check_counted_barrier_waits(asm_text: str, where: str) -> int:
                                        f"a label before {m.group(1)} vector-memory operations")
                 t = items[j][1]
                 op = t.split()[0]
-                if op.startswith("global_load_lds") or op.startswith("buffer_load_lds"):
+                if _loads_to_lds(t):
                     raise RuntimeError(f"{where}: {fname}: counted barrier wait '{text}' would leave "
                                        f"a direct-to-LDS load in flight: {t}")
                 if op.startswith(("s_branch", "s_cbranch", "s_setpc")):

@@ -93,7 +93,7 @@ bool checkpoint_aligned(const ssd_block_checkpoint_t *c, int n) {
 
 // --------------------------------------------------------- 4-bit operands
 
-constexpr int64_t kFewTokens = 64;     // matrix instructions of 16 tokens, up to four a wave
+constexpr int64_t kFewTokens = 32;     // one or two matrix instructions of 16 tokens a wave
 constexpr int64_t kFewQuantised = 16;  // the few-token kernel quantises by itself up to here
 
 int64_t kblocks_of(const ssd_mx4_shape_t *s) { return (s->columns + 127) / 128; }

@@ -3,6 +3,9 @@
 // instructions, which multiply 32 columns of e2m1 codes by both blocks' scales
 // and sum in fp32.  The weights are the instruction's first operand, so that a
 // lane's results are neighbouring columns of one token.
+#include <algorithm>
+#include <type_traits>
+
 #include "ssd_mx4.hpp"
 #include "ssd_tiles.hpp"
 
@@ -115,186 +118,405 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs 
 
 // ------------------------------------------------------------- many tokens
 //
-// A workgroup of four waves owns BM tokens x BN outputs and walks the columns
-// 128 at a time: the codes and scales of three such steps are in LDS, loaded
-// there directly, two steps ahead.  32x32x64: lane l brings row l % 32 and one
-// block of 32 columns of either operand; which block goes into which of a step's two
-// instructions is free as long as both operands agree, so lanes 32 .. 63 take
-// blocks 2 and 3 and a lane's operands are 32 consecutive bytes and two
-// neighbouring scale bytes.  Rows of 64 bytes hold their 16-byte pieces at
-// piece ^ (row / 2 % 4), so that eight consecutive rows at one piece meet eight
-// different bank groups.
+// 32x32x64: lane l brings row l % 32 and one block of 32 columns of either
+// operand; which block goes into which instruction is free as long as both
+// operands agree.  Operands go through LDS, loaded there directly, in rows of
+// SEG bytes whose 16-byte pieces lie at piece ^ (row / (16 / pieces) % pieces):
+// 16 consecutive rows at one piece meet 16 different bank groups.
 
-template <int BM, int BN>
-struct Mx4Stage {
-    static constexpr int kCodes = (BM + BN) * 64;          // tokens, then weights
-    static constexpr int kScales = (BM + BN) * 4;
-    static constexpr int kBytes = kCodes + kScales;
-    static constexpr int kCodeLoads = (BM + BN) / 16 / 4;  // 1 KB each, of each wave
-    static constexpr int kScaleParts = (BM + BN) / 64;     // 64 words each
-    static constexpr int kScaleLoads = (kScaleParts + 3) / 4;
-    static constexpr int kLoads = kCodeLoads + kScaleLoads;
+// An LDS access of any type.
+typedef i32x4 __attribute__((may_alias)) any_i32x4;
+
+template <typename OUT>
+__device__ inline void put4(uint8_t *to, const float (&f)[4]) {
+    if constexpr (sizeof(OUT) == 4) {
+        *(any_i32x4 *)to = i32x4{__float_as_int(f[0]), __float_as_int(f[1]), __float_as_int(f[2]), __float_as_int(f[3])};
+    } else {
+        typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), may_alias));
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        *(any_u32x2 *)to = __builtin_bit_cast(any_u32x2, __builtin_convertvector(f4{f[0], f[1], f[2], f[3]}, bf16x4));
+    }
+}
+
+// A 16-byte piece of a row of y, `left` outputs before the row's end; a lane
+// past the last row or output stores nothing (its offset is outside ys).
+template <typename OUT>
+__device__ inline void store_piece(__amdgpu_buffer_rsrc_t ys, uint32_t at, int left, i32x4 v, bool wide) {
+    constexpr int V = 16 / (int)sizeof(OUT);
+    if (wide) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, ys, left > 0 ? at : 0xffffffffu, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const uint32_t ok = left > e ? at + e * (uint32_t)sizeof(OUT) : 0xffffffffu;
+            if constexpr (sizeof(OUT) == 4) __builtin_amdgcn_raw_buffer_store_b32(v[e], ys, ok, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2))), ys, ok, 0, 0);
+        }
+    }
+}
+
+// A descriptor whose bound is used: rows past an operand's last are read as 0.
+__device__ inline __amdgpu_buffer_rsrc_t bounded(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00027000);
+}
+
+// A wave's sums of a 32 x 32 tile: lane l holds token l % 32 and outputs
+// 8 q + 4 (l / 32) + e.  On their way out they are put into LDS in chunks of 32
+// tokens x 64 bytes (all of the tile's outputs in bf16, a half in fp32), 16-byte
+// pieces at piece ^ (token / 4 % 4), and read back in whole rows.
+constexpr int kChunk = 2048;
+
+template <typename OUT>
+struct Mx4Chunk {
+    static constexpr int kGroups = sizeof(OUT) == 2 ? 4 : 2;   // of 8 outputs
+    static constexpr int kPerTile = 4 / kGroups;
+    static constexpr int V = 16 / (int)sizeof(OUT);            // outputs of a piece
+
+    static __device__ inline void put(uint8_t *to, const f32x16 &s, int part) {
+        const int r = threadIdx.x % 32, g = threadIdx.x / 32 % 2;
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+            const int e = 4 * (part * kGroups + q), byte = (8 * q + 4 * g) * (int)sizeof(OUT);
+            put4<OUT>(to + r * 64 + ((byte / 16) ^ (r / 4 % 4)) * 16 + byte % 16, {s[e], s[e + 1], s[e + 2], s[e + 3]});
+        }
+    }
+
+    // To y's rows from ys on; `row` the chunk's first one, n0 its tile's first
+    // output and `left` what is left of the row from there.
+    static __device__ inline void get(const uint8_t *from, __amdgpu_buffer_rsrc_t ys, int pitch, int row, int n0, int left,
+                                      int part, bool wide) {
+        const int lane = threadIdx.x % 64;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int t = p * 16 + lane / 4, n = part * kGroups * 8 + lane % 4 * V;
+            const i32x4 v = *(const any_i32x4 *)(from + t * 64 + ((lane % 4) ^ (t / 4 % 4)) * 16);
+            const uint32_t at = ((uint32_t)(row + t) * (uint32_t)pitch + (uint32_t)(n0 + n)) * (uint32_t)sizeof(OUT);
+            store_piece<OUT>(ys, at, left - n, v, wide);
+        }
+    }
 };
 
-template <typename OUT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
-    typedef Mx4Stage<BM, BN> ST;
-    constexpr int TM = WM / 32, TN = WN / 32;
-    static_assert((BM / WM) * (BN / WN) == 4, "four waves");
-    constexpr int kEpilogue = 4 * 32 * (WN * (int)sizeof(OUT) + 16);
-    constexpr int kLds = 3 * ST::kBytes > kEpilogue ? 3 * ST::kBytes : kEpilogue;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+// Whether 16-byte stores are aligned in y.
+template <typename OUT>
+__device__ inline bool stores_wide(const Mx4ProductArgs &a) {
+    return a.n % (16 / (int)sizeof(OUT)) == 0 && (uintptr_t)a.y % 16 == 0;
+}
+
+// y's rows from t0 on, `rows` of them (none if negative), from output n0 on.
+template <typename OUT>
+__device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const Mx4ProductArgs &a, int64_t t0, int rows, int n0) {
+    return bounded((OUT *)a.y + t0 * a.n + n0,
+                   rows > 0 ? ((uint32_t)rows * (uint32_t)a.n - (uint32_t)n0) * (uint32_t)sizeof(OUT) : 0u);
+}
+
+// Up to 256 columns: one load of everything, one barrier.  A workgroup of four
+// waves owns 64 tokens x 64 outputs.  Bound by y.
+template <typename OUT>
+__global__ __launch_bounds__(256) void mx4_short_kernel(Mx4ProductArgs a, int tiles_n) {
+    constexpr int ROWS = 128, BLOCK = ROWS * 64 + ROWS * 4;   // of 128 columns: codes, scales
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * BLOCK];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wm = wave % (BM / WM), wn = wave / (BM / WM);
-    // `group` rows of tiles at a time, column by column
-    int tm, tn;
-    {
-        const int id = xcd_contiguous(blockIdx.x, gridDim.x);
-        const int per = group * tiles_n, first = id / per * group;
-        const int rows = min(group, tiles_m - first), in = id % per;
-        tm = first + in % rows;
-        tn = in / rows;
-    }
-    const int64_t m0 = (int64_t)tm * BM;
-    const int n0 = tn * BN;
-    const int mleft = (int)min((int64_t)BM, a.m - m0), nleft = min(BN, a.n - n0);
-    const int pitch = a.kblocks * 64;
-    const uint8_t *ab = a.a + m0 * pitch, *wb = a.w + (int64_t)n0 * pitch;
-    const uint32_t *asb = a.as + m0, *wsb = a.ws + n0;
-    // each load's place in its operand: rows past the last repeat it
-    uint32_t code_off[ST::kCodeLoads];
-    uint32_t scale_off[ST::kScaleLoads];
+    const int id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t m0 = (int64_t)(id / tiles_n) * 64;
+    const int n0 = id % tiles_n * 64, pitch = a.kblocks * 64;
+    const int mleft = (int)min((int64_t)64, a.m - m0), nleft = min(64, a.n - n0);
+    const __amdgpu_buffer_rsrc_t as = bounded(a.a + m0 * pitch, (uint32_t)mleft * (uint32_t)pitch);
+    const __amdgpu_buffer_rsrc_t ws = bounded(a.w + (int64_t)n0 * pitch, (uint32_t)nleft * (uint32_t)pitch);
+    for (int kb = 0; kb < a.kblocks; ++kb) {
+        uint8_t *to = lds + kb * BLOCK;
 #pragma unroll
-    for (int i = 0; i < ST::kCodeLoads; ++i) {
-        const int blk = i * 4 + wave;   // 16 rows
-        const bool tok = blk < BM / 16;
-        const int row = (tok ? blk : blk - BM / 16) * 16 + lane / 4;
-        const int piece = (lane % 4) ^ (row / 2 % 4);
-        code_off[i] = (uint32_t)min(row, (tok ? mleft : nleft) - 1) * (uint32_t)pitch + piece * 16;
-    }
-#pragma unroll
-    for (int i = 0; i < ST::kScaleLoads; ++i) {
-        const int part = (i * 4 + wave) % ST::kScaleParts;   // the surplus repeats earlier parts
-        const bool tok = part < BM / 64;
-        const int row = (tok ? part : part - BM / 64) * 64 + lane;
-        scale_off[i] = (uint32_t)min(row, (tok ? mleft : nleft) - 1) * 4u;
-    }
-    auto issue = [&](int kb, int buf) {
-        uint8_t *to = lds + buf * ST::kBytes;
-#pragma unroll
-        for (int i = 0; i < ST::kCodeLoads; ++i) {
-            const int blk = i * 4 + wave;
-            const uint8_t *from = (blk < BM / 16 ? ab : wb) + kb * 64;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + code_off[i]),
-                                             (__attribute__((address_space(3))) void *)(to + blk * 1024), 16, 0, 0);
+        for (int i = 0; i < 2; ++i) {   // 16 rows a load: tokens, weights
+            const int row = wave * 16 + lane / 4;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i ? ws : as, (__attribute__((address_space(3))) void *)(to + (i * 4 + wave) * 1024),
+                                                     16, row * pitch + kb * 64 + ((lane % 4) ^ (row / 4 % 4)) * 16, 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < ST::kScaleLoads; ++i) {
-            const int part = (i * 4 + wave) % ST::kScaleParts;
-            const uint8_t *from = part < BM / 64 ? (const uint8_t *)(asb + (int64_t)kb * a.m)
-                                                 : (const uint8_t *)(wsb + (int64_t)kb * a.n);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + scale_off[i]),
-                                             (__attribute__((address_space(3))) void *)(to + ST::kCodes + part * 256), 4, 0, 0);
+        if (wave < 2) {
+            const __amdgpu_buffer_rsrc_t sc = wave ? bounded(a.ws + (int64_t)kb * a.n + n0, nleft * 4u)
+                                                   : bounded(a.as + (int64_t)kb * a.m + m0, mleft * 4u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(sc, (__attribute__((address_space(3))) void *)(to + ROWS * 64 + wave * 256), 4,
+                                                     lane * 4, 0, 0, 0);
         }
-    };
-    const int r = lane % 32, g = lane / 32;
-    // where the lane's operands lie in a step's LDS
-    uint32_t tok_at[2], wgt_at[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int piece = (2 * g + s) ^ (r / 2 % 4);
-        tok_at[s] = (wm * WM + r) * 64 + piece * 16;
-        wgt_at[s] = (BM + wn * WN + r) * 64 + piece * 16;
     }
-    const uint32_t tok_scale = ST::kCodes + (wm * WM + r) * 4, wgt_scale = ST::kCodes + (BM + wn * WN + r) * 4;
-    // the sums start at the bias: a lane holds outputs 32 j + 8 q + 4 g + e
-    f32x16 acc[TN][TM] = {};
-    const int nb = n0 + wn * WN;
+    const int wm = wave % 2, wn = wave / 2, r = lane % 32, g = lane / 32;
+    f32x16 acc = {};
     if (a.bias) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float b = a.bias[min(nb + 32 * j + 8 * (e / 4) + 4 * g + e % 4, a.n - 1)];
-#pragma unroll
-                for (int i = 0; i < TM; ++i) acc[j][i][e] = b;
-            }
+        for (int e = 0; e < 16; ++e) acc[e] = a.bias[min(n0 + 32 * wn + 8 * (e / 4) + 4 * g + e % 4, a.n - 1)];
     }
-    auto compute = [&](int buf) {
-        const uint8_t *at = lds + buf * ST::kBytes;
-        int ts[TM], wsc[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) ts[i] = (int)(*(const uint32_t *)(at + tok_scale + i * 128) >> (16 * g));
-#pragma unroll
-        for (int j = 0; j < TN; ++j) wsc[j] = (int)(*(const uint32_t *)(at + wgt_scale + j * 128) >> (16 * g));
+    vmem_lds_sync();
+    for (int kb = 0; kb < a.kblocks; ++kb) {
+        const uint8_t *at = lds + kb * BLOCK;
+        const int tr = wm * 32 + r, wr = 64 + wn * 32 + r;
+        // lanes 0 .. 31 take blocks 0 and 1 of the four, lanes 32 .. 63 the others
+        const int ts = (int)(*(const uint32_t *)(at + ROWS * 64 + tr * 4) >> (16 * g));
+        const int wsc = (int)(*(const uint32_t *)(at + ROWS * 64 + wr * 4) >> (16 * g));
+        i32x4 t[2], w[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            i32x4 t[TM], w[TN];
+            t[s] = *(const i32x4 *)(at + tr * 64 + ((2 * g + s) ^ (tr / 4 % 4)) * 16);
+            w[s] = *(const i32x4 *)(at + wr * 64 + ((2 * g + s) ^ (wr / 4 % 4)) * 16);
+        }
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[0]), mx4_operand(t[0]), acc, 4, 4, 0, wsc, 0, ts);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[1]), mx4_operand(t[1]), acc, 4, 4, 1, wsc, 1, ts);
+    }
+    lds_sync();
+    typedef Mx4Chunk<OUT> CH;
+    uint8_t *mine = lds + wave * kChunk;
+    const __amdgpu_buffer_rsrc_t ys = rows_of_y<OUT>(a, m0, mleft, n0);
+    const bool wide = stores_wide<OUT>(a);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) w[j] = *(const i32x4 *)(at + wgt_at[s] + j * 2048);
+    for (int part = 0; part < CH::kPerTile; ++part) {
+        CH::put(mine, acc, part);
+        CH::get(mine, ys, a.n, wm * 32, wn * 32, nleft - wn * 32, part, wide);
+    }
+}
+
+// More columns: a workgroup owns BM tokens x BN outputs at a time and walks
+// them 256 columns a stage, then goes on to its next tile without a pause: one
+// stage is in LDS, the next one on its way.  What shapes it, measured for 16384 x
+// 10576 x 2560 (a 16384^3 bf16 product of the library reaches 1.6 PFLOP/s here):
+//  - The matrix units draw so much power on random operands that they alone
+//    reach 6.5 PFLOP/s (136 us), 8.9 on constant ones.
+//  - L2 is read in lines of 128 bytes: rows of 64 bytes a stage take 137 us to
+//    bring 256 x 256 tiles into LDS, rows of 128 bytes 87 us; 128 x 128 tiles 145.
+//  - A wave that waits to issue a load issues no matrix instruction, and what
+//    the compiler moves across a barrier overlaps nothing.  So one matrix
+//    instruction, one operand read and at most a few loads follow each other
+//    in the order written (299 us without that, 189 with, no result stored).
+//  - Loads and stores of a wave complete in order, and all tiles end at about the
+//    same time: waves that store must not load.  The first half of the waves
+//    loads every stage, the other half stores every result, its partner's
+//    chunk by chunk through LDS (293 us before, 262 after).
+//  - `group` rows of tiles column by column, four of them: neighbouring pieces
+//    of y's rows meet in one XCD's L2 (262 us with eight, 218 with four).
+// The stage of an odd last 128 columns is the last 256 once more with the scales
+// of the first half, which has been taken, at 2^-127: a product below 2^-240 in
+// place of each, which fp32 sums round away.
+template <int BM, int BN>
+struct Mx4Stage {
+    static constexpr int kRows = BM + BN;
+    static constexpr int kCodes = kRows * 128;
+    static constexpr int kBytes = kCodes + kRows * 8;   // codes, then two words of scales a row, block by block
+};
+
+struct Mx4Tile {
+    const uint8_t *a, *w;
+    const uint32_t *as, *ws;
+    int m, n;      // rows of either operand, at most BM and BN
+    int64_t m0;
+    int n0;
+};
+
+template <typename OUT, int BM, int BN, int WM, int WN, int PERCU>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), PERCU * (BM / WM) * (BN / WN) / 4)
+void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
+    typedef Mx4Stage<BM, BN> ST;
+    typedef Mx4Chunk<OUT> CH;
+    constexpr int W = (BM / WM) * (BN / WN), LW = W / 2;   // waves, and those of them that load
+    constexpr int TM = WM / 32, TN = WN / 32, N = TN * TM, READS = TN + TM;
+    constexpr int LA = BM / 8 / LW, LB = BN / 8 / LW, PARTS = ST::kRows / 64, LS = 2 * PARTS / LW, LOADS = LA + LB + LS;
+    static_assert(LA * 8 * LW == BM && LB * 8 * LW == BN && LS * LW == 2 * PARTS, "whole loads");
+    // Loads after the barrier that frees their buffer, and before the next one
+    // that waits for them; reads and loads after each matrix instruction.
+    constexpr int RP = (READS + N - 1) / N, LP = (LOADS * 6 / 10 + N - 1) / N, FIRST = LP * N < LOADS ? LP * N : LOADS,
+                  LQ = (LOADS - FIRST + N - 1) / N;
+    constexpr int CHUNKS = N * CH::kPerTile;
+    // chunks on their way out: two of each loading wave, one of each storing one
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * ST::kBytes + 3 * LW * kChunk];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave % (BM / WM), wn = wave / (BM / WM);
+    const int pitch = a.kblocks * 64, stages = (a.kblocks + 1) / 2;   // stages >= 2
+    // each XCD a range of the tiles by its share of the workgroups, dealt to them in turn
+    const int xcd = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8, nlocal = each + (xcd < more);
+    const int64_t tiles = (int64_t)tiles_m * tiles_n;
+    auto before = [&](int x) { return (int)(tiles * (x * each + min(x, more)) / (int)gridDim.x); };
+    const int begin = before(xcd) + blockIdx.x / 8, end = before(xcd + 1);
+    if (begin >= end) return;
+    auto place = [&](int id) {
+        const int per = group * tiles_n, first = id / per * group;
+        const int rows = min(group, tiles_m - first), in = id % per;
+        Mx4Tile t;
+        t.m0 = (int64_t)(first + in % rows) * BM;
+        t.n0 = in / rows * BN;
+        t.m = (int)min((int64_t)BM, a.m - t.m0);
+        t.n = min(BN, a.n - t.n0);
+        t.a = a.a + t.m0 * pitch;
+        t.w = a.w + (int64_t)t.n0 * pitch;
+        t.as = a.as + t.m0;
+        t.ws = a.ws + t.n0;
+        return t;
+    };
+    // ---- loads: 8 rows of codes, or 64 words of scales, each
+    const int lrow = wave * 8 + lane / 8;
+    const uint32_t code_at = (uint32_t)lrow * (uint32_t)pitch + ((lane % 8) ^ (lrow / 2 % 8)) * 16;
+    auto load = [&](int i, const Mx4Tile &t, int st, int buf) {
+        uint8_t *to = lds + buf * ST::kBytes;
+        const int byte0 = min(st * 128, pitch - 128);
+        if (i < LA + LB) {
+            const bool tok = i < LA;
+            const int k = tok ? i : i - LA;
+            const __amdgpu_buffer_rsrc_t rs = bounded(tok ? t.a : t.w, (uint32_t)(tok ? t.m : t.n) * (uint32_t)pitch);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (__attribute__((address_space(3))) void *)(to + (i * LW + wave) * 1024), 16,
+                code_at + (uint32_t)(k * LW * 8 * pitch + byte0), 0, 0, 0);
+        } else {
+            const int p = (i - LA - LB) * LW + wave, h = p / PARTS, part = p % PARTS;
+            const bool tok = part < BM / 64;
+            const int kb = byte0 / 64 + h;
+            const uint32_t *from = tok ? t.as + (int64_t)kb * a.m : t.ws + (int64_t)kb * a.n;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                bounded(from, (uint32_t)(tok ? t.m : t.n) * 4u),
+                (__attribute__((address_space(3))) void *)(to + ST::kCodes + h * ST::kRows * 4 + part * 256), 4,
+                (uint32_t)((tok ? part : part - BM / 64) * 64 + lane) * 4u, 0, 0, 0);
+        }
+    };
+    // ---- operands: lanes 0 .. 31 take the stage's first 128 columns, lanes 32 ..
+    // 63 the others; step s of four multiplies each one's block s
+    const int r = lane % 32, g = lane / 32;
+    uint32_t tok_at[4];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) t[i] = *(const i32x4 *)(at + tok_at[s] + i * 2048);
+    for (int s = 0; s < 4; ++s) tok_at[s] = (wm * WM + r) * 128 + ((4 * g + s) ^ (r / 2 % 8)) * 16;
+    const int to_weights = (BM + wn * WN - wm * WM) * 128;
+    const uint32_t tok_scale = ST::kCodes + (g * ST::kRows + wm * WM + r) * 4;
+    const uint32_t wgt_scale = ST::kCodes + (g * ST::kRows + BM + wn * WN + r) * 4;
+    i32x4 t[2][TM], w[2][TN];
+    int ts[TM], ws[TN], ts_next[TM], ws_next[TN];
+    auto read = [&](int i, int buf, int step, int set) {
+        const uint8_t *at = lds + buf * ST::kBytes + tok_at[step];
+        if (i < TN) w[set][i] = *(const i32x4 *)(at + to_weights + i * 4096);
+        else if (i < READS) t[set][i - TN] = *(const i32x4 *)(at + (i - TN) * 4096);
+    };
+    auto read_scale = [&](int i, int buf) {
+        const uint8_t *at = lds + buf * ST::kBytes;
+        if (i < TN) ws_next[i] = *(const int *)(at + wgt_scale + i * 128);
+        else if (i < READS) ts_next[i - TN] = *(const int *)(at + tok_scale + (i - TN) * 128);
+    };
+    auto scales_of = [&](int st) {
+        const bool taken = g == 0 && 2 * st + 1 == a.kblocks;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) ts[i] = taken ? 0 : ts_next[i];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) ws[j] = taken ? 0 : ws_next[j];
+    };
+    f32x16 acc[TN][TM];
+    auto multiply = [&](auto step, int set, auto &&between) {
+        constexpr int S = decltype(step)::value;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int j = k / TM, i = k % TM;
+            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[set][j]), mx4_operand(t[set][i]),
+                                                                        acc[j][i], 4, 4, S, ws[j], S, ts[i]);
+            between(k);
+            __builtin_amdgcn_sched_barrier(0x6);   // only arithmetic moves across
+        }
+    };
+    const bool wide = stores_wide<OUT>(a);
+    auto walk = [&](auto role) {
+        constexpr bool LOADER = decltype(role)::value;
+        Mx4Tile cur = place(begin);
+        if (LOADER) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(i, cur, 0, 0);
+            vmem_lds_sync();
+#pragma unroll
+            for (int i = 0; i < FIRST; ++i) load(i, cur, 1, 1);
+        } else {
+            lds_sync();
+        }
+        int buf = 0;
+#pragma unroll
+        for (int i = 0; i < READS; ++i) {
+            read(i, 0, 0, 0);
+            read_scale(i, 0);
+        }
+        scales_of(0);
+        for (int tile = begin; tile < end; tile += nlocal) {
+            const Mx4Tile next = place(tile + nlocal < end ? tile + nlocal : tile);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    if (s == 0)
-                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[j]), mx4_operand(t[i]),
-                                                                                    acc[j][i], 4, 4, 0, wsc[j], 0, ts[i]);
-                    else
-                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[j]), mx4_operand(t[i]),
-                                                                                    acc[j][i], 4, 4, 1, wsc[j], 1, ts[i]);
-                }
-        }
-    };
-    const int last = a.kblocks - 1;
-    issue(0, 0);
-    issue(min(1, last), 1);
-    vmem_lds_sync_lookahead<ST::kLoads, 0>();
-    int buf = 0, ahead = 2;
-    for (int kb = 0; kb <= last; ++kb) {
-        issue(min(kb + 2, last), ahead);   // (past the end: the last step again, into a buffer nothing reads)
-        compute(buf);
-        vmem_lds_sync_lookahead<ST::kLoads, 1>();
-        buf = buf == 2 ? 0 : buf + 1;
-        ahead = ahead == 2 ? 0 : ahead + 1;
-    }
-    vmem_lds_sync();
-    // 32 tokens at a time through the wave's own part of LDS, so that a row of
-    // the wave's WN outputs is stored in one piece.
-    constexpr int kRow = WN * (int)sizeof(OUT) + 16;
-    uint8_t *mine = lds + wave * 32 * kRow;
-    constexpr int V = 16 / (int)sizeof(OUT), PER = WN / V;   // 16-byte pieces of a row
-    const bool wide = a.n % V == 0 && (uintptr_t)a.y % 16 == 0;
-    const int col = lane % PER * V;
+                for (int i = 0; i < TM; ++i) acc[j][i] = f32x16{};
+            if (a.bias) {
+                // lane: outputs 32 j + 8 q + 4 g + e
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+                for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+                    for (int e = 0; e < 16; ++e) {
+                        const float b = a.bias[min(cur.n0 + wn * WN + 32 * j + 8 * (e / 4) + 4 * g + e % 4, a.n - 1)];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float o[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-                store_pack<OUT, 4>(mine + r * kRow + (32 * j + 8 * q + 4 * g) * (int)sizeof(OUT), o);
+                        for (int i = 0; i < TM; ++i) acc[j][i][e] += b;
+                    }
             }
-        lds_sync();
+            for (int st = 0; st < stages; ++st) {
+                auto reads = [&](int k, int step, int set) {
 #pragma unroll
-        for (int p = 0; p < 32 * PER / 64; ++p) {
-            const int row = p * (64 / PER) + lane / PER;
-            const int64_t t = m0 + wm * WM + i * 32 + row;
-            const Pack<OUT, V> v = *(const Pack<OUT, V> *)(mine + row * kRow + col * (int)sizeof(OUT));
-            if (t < a.m) {
-                OUT *y = (OUT *)a.y + t * a.n + nb + col;
-                if (wide && nb + col + V <= a.n) {
-                    *(Pack<OUT, V> *)y = v;
+                    for (int q = 0; q < RP; ++q) read(k * RP + q, buf, step, set);
+                };
+                // The stage whose last loads begin before this one's barrier and
+                // the one whose first loads begin after it: of this tile or, in
+                // its place at the end of the walk this tile again, the next.
+                auto ahead = [&](int n, int &of) {
+                    const bool over = st + n >= stages;
+                    of = over ? st + n - stages : st + n;
+                    return Mx4Tile{over ? next.a : cur.a, over ? next.w : cur.w, over ? next.as : cur.as,
+                                   over ? next.ws : cur.ws, over ? next.m : cur.m, over ? next.n : cur.n, 0, 0};
+                };
+                int s1, s2;
+                const Mx4Tile t1 = ahead(1, s1), t2 = ahead(2, s2);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(std::integral_constant<int, 0>{}, 0, [&](int k) {
+                    reads(k, 1, 1);
+#pragma unroll
+                    for (int q = 0; q < LQ; ++q)
+                        if (LOADER && FIRST + k * LQ + q < LOADS) load(FIRST + k * LQ + q, t1, s1, buf ^ 1);
+                });
+                multiply(std::integral_constant<int, 1>{}, 1, [&](int k) { reads(k, 2, 0); });
+                multiply(std::integral_constant<int, 2>{}, 0, [&](int k) { reads(k, 3, 1); });
+                // every wave has read this stage, and the next one has landed
+                if (LOADER) vmem_lds_sync();
+                else lds_sync();
+                __builtin_amdgcn_sched_barrier(0);
+                buf ^= 1;
+                multiply(std::integral_constant<int, 3>{}, 1, [&](int k) {
+                    reads(k, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < RP; ++q) read_scale(k * RP + q, buf);
+#pragma unroll
+                    for (int q = 0; q < LP; ++q)
+                        if (LOADER && k * LP + q < FIRST) load(k * LP + q, t2, s2, buf ^ 1);
+                });
+                scales_of(st + 1 < stages ? st + 1 : 0);
+            }
+            // ---- out, both of a pair's chunks by the storing wave: a chunk of the
+            // loading one is written again two barriers on
+            uint8_t *out = lds + 2 * ST::kBytes;
+            auto store = [&](int c, const uint8_t *from, int of) {
+                const int i = c / CH::kPerTile / TN, j = c / CH::kPerTile % TN;
+                const int om = of % (BM / WM) * WM, on = of / (BM / WM) * WN + 32 * j;
+                CH::get(from, rows_of_y<OUT>(a, cur.m0 + om, min(WM, cur.m - om), cur.n0), a.n, 32 * i, on, cur.n - on,
+                        c % CH::kPerTile, wide);
+            };
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int i = c / CH::kPerTile / TN, j = c / CH::kPerTile % TN, part = c % CH::kPerTile;
+                if (LOADER) {
+                    CH::put(out + (wave * 2 + c % 2) * kChunk, acc[j][i], part);
+                    lds_sync();
                 } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (nb + col + e < a.n) y[e] = v.v[e];
+                    uint8_t *mine = out + (LW + wave) * kChunk;
+                    CH::put(mine, acc[j][i], part);
+                    store(c, mine, wave);
+                    lds_sync();
+                    store(c, out + ((wave - LW) * 2 + c % 2) * kChunk, wave - LW);
                 }
             }
+            cur = next;
         }
-        lds_sync();
-    }
+        // what was loaded for a tile that does not follow
+        if (LOADER) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    };
+    if (wave < LW) walk(std::true_type{});
+    else walk(std::false_type{});
 }
 
 // ---------------------------------------------------------------- launches
@@ -314,30 +536,34 @@ static void mx4_few_out(bool wide, const Mx4ProductArgs &a, hipStream_t stream) 
     if (a.x) {
         wide ? mx4_few_launch<OUT, OUT, 1, true>(a, stream) : mx4_few_launch<OUT, OUT, 1, false>(a, stream);
     } else {
-        switch ((a.m + 15) / 16) {
-        case 1: mx4_few_launch<uint8_t, OUT, 1, true>(a, stream); break;
-        case 2: mx4_few_launch<uint8_t, OUT, 2, true>(a, stream); break;
-        default: mx4_few_launch<uint8_t, OUT, 4, true>(a, stream);
-        }
+        a.m <= 16 ? mx4_few_launch<uint8_t, OUT, 1, true>(a, stream) : mx4_few_launch<uint8_t, OUT, 2, true>(a, stream);
     }
 }
 
-template <typename OUT, int BM, int BN, int WM, int WN>
+template <typename OUT, int BM, int BN, int WM, int WN, int PERCU>
 static void mx4_tile_launch(const Mx4ProductArgs &a, hipStream_t stream) {
     const int tm = (int)((a.m + BM - 1) / BM), tn = (a.n + BN - 1) / BN;
-    hipLaunchKernelGGL((mx4_tile_kernel<OUT, BM, BN, WM, WN>), dim3((unsigned)((int64_t)tm * tn)), dim3(256), 0, stream, a, tm,
-                       tn, 8);
+    const int64_t grid = std::min((int64_t)tm * tn, (int64_t)PERCU * a.cus);
+    hipLaunchKernelGGL((mx4_tile_kernel<OUT, BM, BN, WM, WN, PERCU>), dim3((unsigned)grid), dim3(64 * (BM / WM) * (BN / WN)), 0,
+                       stream, a, tm, tn, 4);
 }
 
+// The largest tile that still occupies the device, in us for m x 2560 x 5120
+// and m x 10576 x 2560 with tiles of 256 / 128 / 64: m = 4096: 33 41 57 and 60 70
+// 117; 2048: 30 24 31 and 38 38 59; 1024: 28 16 19 and 22 23 34; 512: 46 15
+// 14 and 30 20 19; 256: 46 15 11 and 28 16 11.  So 256 from 5/8 of the compute
+// units on, 64 while one round of three a compute unit holds them all.
 template <typename OUT>
 static void mx4_tile_out(const Mx4ProductArgs &a, hipStream_t stream) {
-    const auto tiles = [&](int bm, int bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
-    if (tiles(256, 128) >= 2 * (int64_t)a.cus)
-        mx4_tile_launch<OUT, 256, 128, 128, 64>(a, stream);
-    else if (tiles(128, 128) >= 2 * (int64_t)a.cus)
-        mx4_tile_launch<OUT, 128, 128, 64, 64>(a, stream);
+    const auto tiles = [&](int b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b); };
+    if (a.kblocks <= 2)
+        hipLaunchKernelGGL((mx4_short_kernel<OUT>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
+    else if (8 * tiles(256) >= 5 * (int64_t)a.cus)
+        mx4_tile_launch<OUT, 256, 256, 128, 64, 1>(a, stream);
+    else if (tiles(64) > 3 * (int64_t)a.cus)
+        mx4_tile_launch<OUT, 128, 128, 64, 64, 2>(a, stream);
     else
-        mx4_tile_launch<OUT, 64, 64, 32, 32>(a, stream);
+        mx4_tile_launch<OUT, 64, 64, 32, 32, 3>(a, stream);
 }
 
 void launch_mx4_product(bool bf16_out, bool wide, bool few, const Mx4ProductArgs &a, hipStream_t stream) {

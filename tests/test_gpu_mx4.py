@@ -124,7 +124,8 @@ def operands(gen, m, n, k, exact):
 PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 17, 300), (2, 33, 129), (15, 100, 2560), (16, 130, 640), (17, 64, 256), (31, 47, 1000),
             (32, 64, 128), (33, 200, 500), (64, 129, 384), (65, 64, 128), (65, 1, 77), (100, 333, 1477), (128, 128, 1024),
             (129, 257, 200), (700, 1000, 256), (2000, 1030, 640), (1501, 1001, 1477), (2500, 2600, 300), (4100, 4200, 129),
-            (1, 9000, 256), (20, 9001, 256), (5000, 20, 64)]
+            (1, 9000, 256), (20, 9001, 256), (5000, 20, 64), (4100, 4200, 700), (3333, 3001, 385), (3400, 2900, 1024),
+            (200, 70, 2900), (66, 5000, 257), (1300, 2111, 900), (9000, 1000, 300), (770, 8500, 513)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -138,7 +139,7 @@ def test_matmul_exact_sums(m, n, k):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("bias", [False, True])
-@pytest.mark.parametrize("m,n,k", [c for c in PRODUCTS if c[0] * c[1] < 3_000_000])
+@pytest.mark.parametrize("m,n,k", [c for c in PRODUCTS if c[0] * c[1] * c[2] < 3_000_000_000])
 def test_matmul_and_linear(m, n, k, bias, dtype):
     gen = torch.Generator().manual_seed(m * 3 + n + k)
     io = TYPES[dtype]
