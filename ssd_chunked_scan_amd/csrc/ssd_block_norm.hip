@@ -49,28 +49,42 @@ __device__ inline void row_sums(float (&v)[N], float *lds) {
     }
 }
 
-// A row's values as e4m3 with a scale per 128 columns: q at the row's start, sc
-// its scales.
+// A row of a tensor through a buffer descriptor that ends with its last column:
+// what lies past it is read as 0 and not written, so that no lane needs a
+// branch, and a tensor that is not given (bytes 0) reads as 0 throughout.
+__device__ inline __amdgpu_buffer_rsrc_t row_of(const void *base, int64_t row, int64_t stride, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(base) + row * stride, 0, bytes, 0x00027000);
+}
+
+// A row's values as e4m3 with a scale per 128 columns.
 template <int V, int K>
-__device__ inline void store_checkpoint(uint8_t *q, float *sc, const float (&val)[K][V], int tid, int nthr, int npack) {
+__device__ inline void store_checkpoint(__amdgpu_buffer_rsrc_t q, __amdgpu_buffer_rsrc_t sc, const float (&val)[K][V], int tid,
+                                        int nthr) {
     constexpr int PER = V == 1 ? 2 : 1, LANES = V == 1 ? 64 : 128 / V;
 #pragma unroll
     for (int k = 0; k < K; k += PER) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if (pack_at<V>(k + j, tid, nthr) < npack) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) m = max(m, abs_bits(val[k + j][v]));
-            }
+            for (int v = 0; v < V; ++v) m = max(m, abs_bits(val[k + j][v]));
         const float mx = __uint_as_float(max(lanes_max<LANES>(m), kMinMost));
         const float inv = 448.f / mx;
         const int p0 = pack_at<V>(k, tid, nthr);
-        if (tid % LANES == 0 && p0 < npack) sc[p0 * V / 128] = mx / 448.f;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(mx / 448.f), sc,
+                                              tid % LANES == 0 ? (uint32_t)(p0 * V / 128) * 4u : 0xffffffffu, 0, 0);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int p = pack_at<V>(k + j, tid, nthr);
-            if (p < npack) store_e4m3<V>(q + p * V, val[k + j], inv);
+            const uint32_t at = (uint32_t)(pack_at<V>(k + j, tid, nthr) * V);
+            uint8_t code[V];
+            store_e4m3<V>(code, val[k + j], inv);
+            if constexpr (V == 1) {
+                __builtin_amdgcn_raw_buffer_store_b8(code[0], q, at, 0, 0);
+            } else if constexpr (V == 4) {
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(Pack<uint32_t, 1>, code).v[0], q, at, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(Words<8>::type, code), q, at, 0, 0);
+            }
         }
     }
 }
@@ -83,18 +97,19 @@ struct Kept {
 };
 
 template <int V>
-__device__ inline Kept<V> load_kept(const uint8_t *q, const float *sc, int p) {
+__device__ inline Kept<V> load_kept(__amdgpu_buffer_rsrc_t q, __amdgpu_buffer_rsrc_t sc, int p) {
     Kept<V> r;
+    const uint32_t at = (uint32_t)(p * V);
     if constexpr (V == 8) {
-        const Pack<uint32_t, 2> t = *(const Pack<uint32_t, 2> *)(q + p * V);
-        r.w[0] = t.v[0];
-        r.w[1] = t.v[1];
+        const Words<8>::type t = __builtin_amdgcn_raw_buffer_load_b64(q, at, 0, 0);
+        r.w[0] = t[0];
+        r.w[1] = t[1];
     } else if constexpr (V == 4) {
-        r.w[0] = *(const uint32_t *)(q + p * V);
+        r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(q, at, 0, 0);
     } else {
-        r.w[0] = q[p];
+        r.w[0] = __builtin_amdgcn_raw_buffer_load_b8(q, at, 0, 0);
     }
-    r.scale = sc[p * V / 128];
+    r.scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sc, at / 128u * 4u, 0, 0));
     return r;
 }
 
@@ -115,63 +130,62 @@ __device__ inline void kept_values(const Kept<V> &r, float (&f)[V]) {
     }
 }
 
+// The weights of a thread's columns: post * scale and pre, 1 where not given.
+template <int V>
+__device__ inline void block_weights(const BlockArgs &a, int p, float (&w1)[V], float (&w2)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = min(p * V + v, a.columns - 1);
+        w1[v] = (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
+        w2[v] = a.pre ? a.pre[c] : 1.f;
+    }
+}
+
 template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs a) {
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     constexpr int RPB = WAVE ? 4 : 1;   // rows a workgroup takes at a time
+    constexpr int E = (int)sizeof(IO);
     __shared__ float lds[2][16];
     const int tid = WAVE ? threadIdx.x % 64 : threadIdx.x, nthr = WAVE ? 64 : blockDim.x;
-    const int npack = a.columns / V, nscale = (a.columns + 127) / 128;
+    const int nscale = (a.columns + 127) / 128, bytes = a.columns * E, dense = bytes;
     const float inv_n = 1.f / (float)a.columns;
     const int64_t step = (int64_t)gridDim.x * RPB;
-    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x / 64 : 0);
-    Pack<IO, V> xr[K], rr[K], zr[K], xn[K], rn[K], zn[K];
-    auto load = [&](int64_t r, Pack<IO, V> (&x)[K], Pack<IO, V> (&s)[K], Pack<IO, V> (&z)[K]) {
-        const char *xb = (const char *)a.x + r * a.xs, *sb = (const char *)a.residual + r * a.rs;
-        const char *zb = (const char *)a.z + r * a.zs;
+    int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
+    if (row >= a.rows) return;   // (without WAVE a workgroup has a row)
+    R xr[K], rr[K], zr[K], xn[K], rn[K], zn[K];
+    auto load = [&](int64_t r, R (&x)[K], R (&s)[K], R (&z)[K]) {
+        const __amdgpu_buffer_rsrc_t xb = row_of(a.x, r, a.xs, bytes), sb = row_of(a.residual, r, a.rs, bytes);
+        const __amdgpu_buffer_rsrc_t zb = row_of(a.z, r, a.zs, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                const int64_t off = p * (V * (int)sizeof(IO));
-                x[k] = load_pack<IO, V>(xb + off);
-                s[k] = load_pack<IO, V>(sb + off);
-                if (GATE) z[k] = load_pack<IO, V>(zb + off);
-            }
+            const uint32_t at = (uint32_t)(pack_at<V>(k, tid, nthr) * (V * E));
+            x[k] = buffer_load<R>(xb, at, 0);
+            s[k] = buffer_load<R>(sb, at, 0);
+            if (GATE) z[k] = buffer_load<R>(zb, at, 0);
         }
     };
-    if (row < a.rows) load(row, xr, rr, zr);
+    load(row, xr, rr, zr);
     constexpr bool HOLD = K * V <= 8;   // the weights stay in registers
-    auto weight1 = [&](int p, int v) {
-        const int c = p * V + v;
-        return (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
-    };
-    auto weight2 = [&](int p, int v) { return a.pre ? a.pre[p * V + v] : 1.f; };
-    float w1[HOLD ? K : 1][HOLD ? V : 1], w2[HOLD ? K : 1][HOLD ? V : 1];
+    float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V];
     if constexpr (HOLD) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int p = min(pack_at<V>(k, tid, nthr), npack - 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                w1[k][v] = weight1(p, v);
-                w2[k][v] = weight2(p, v);
-            }
-        }
+        for (int k = 0; k < K; ++k) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
     }
     for (; row < a.rows; row += step) {
-        if (row + step < a.rows) load(row + step, xn, rn, zn);
+        load(min(row + step, a.rows - 1), xn, rn, zn);
         float val[K][V], sum[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (pack_at<V>(k, tid, nthr) < npack) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    val[k][v] = (float)xr[k].v[v];
-                    sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
-                }
+            for (int v = 0; v < V; ++v) {
+                val[k][v] = RW::at(xr[k], v);
+                sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
             }
         if constexpr (CKPT)
-            store_checkpoint<V, K>(a.xq + row * a.columns, a.xsc + row * nscale, val, tid, nthr, npack);
+            store_checkpoint<V, K>(row_of(a.xq, row, a.columns, a.columns), row_of(a.xsc, row, nscale * 4, nscale * 4), val, tid,
+                                   nthr);
         row_sums<WAVE, 1>(sum, lds[0]);
         const float rstd1 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
         if constexpr (CKPT && GATE) {
@@ -179,51 +193,45 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int v = 0; v < V; ++v) z[k][v] = (float)zr[k].v[v];
-            store_checkpoint<V, K>(a.zq + row * a.columns, a.zsc + row * nscale, z, tid, nthr, npack);
+                for (int v = 0; v < V; ++v) z[k][v] = RW::at(zr[k], v);
+            store_checkpoint<V, K>(row_of(a.zq, row, a.columns, a.columns), row_of(a.zsc, row, nscale * 4, nscale * 4), z, tid,
+                                   nthr);
         }
         sum[0] = 0.f;
+        const __amdgpu_buffer_rsrc_t ro = row_of(a.residual_out, row, dense, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                Pack<IO, V> st;
+            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
+            float st[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float w, b = val[k][v] * rstd1;
-                    if constexpr (HOLD) w = w1[k][v];
-                    else w = weight1(p, v);
-                    b *= w;
-                    if (GATE) {
-                        const float z = (float)zr[k].v[v];
-                        b *= z * sigmoid_f32(z);
-                    }
-                    // the stream is kept in the io type, and the second norm
-                    // is of what it holds, which is what backward reads
-                    st.v[v] = (IO)fmaf(a.alpha, (float)rr[k].v[v], b);
-                    val[k][v] = (float)st.v[v];
-                    sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
+            for (int v = 0; v < V; ++v) {
+                float b = val[k][v] * rstd1 * w1[HOLD ? k : 0][v];
+                if (GATE) {
+                    const float z = RW::at(zr[k], v);
+                    b *= z * sigmoid_f32(z);
                 }
-                *(Pack<IO, V> *)((IO *)a.residual_out + row * a.columns + p * V) = st;
+                // the stream is kept in the io type, and the second norm is of
+                // what it holds, which is what backward reads
+                st[v] = (float)(IO)fmaf(a.alpha, RW::at(rr[k], v), b);
+                val[k][v] = st[v];
+                sum[0] = fmaf(st[v], st[v], sum[0]);
             }
+            buffer_store<IO, V>(ro, (uint32_t)(p * (V * E)), 0, st);
         }
         if constexpr (CKPT)
-            store_checkpoint<V, K>(a.sq + row * a.columns, a.ssc + row * nscale, val, tid, nthr, npack);
+            store_checkpoint<V, K>(row_of(a.sq, row, a.columns, a.columns), row_of(a.ssc, row, nscale * 4, nscale * 4), val, tid,
+                                   nthr);
         row_sums<WAVE, 1>(sum, lds[1]);
         const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
+        const __amdgpu_buffer_rsrc_t yb = row_of(a.y, row, dense, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
+            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float w;
-                    if constexpr (HOLD) w = w2[k][v];
-                    else w = weight2(p, v);
-                    val[k][v] = val[k][v] * rstd2 * w;
-                }
-                store_pack<IO, V>((IO *)a.y + row * a.columns + p * V, val[k]);
-            }
+            for (int v = 0; v < V; ++v) val[k][v] = val[k][v] * rstd2 * w2[HOLD ? k : 0][v];
+            buffer_store<IO, V>(yb, (uint32_t)(p * (V * E)), 0, val[k]);
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -238,58 +246,57 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
 // two sums in registers; each leaves a row of parts [2][columns]: m, dpre.
 template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_bwd_kernel(BlockArgs a) {
+    typedef Raw<IO, V> RW;
+    typedef typename RW::type R;
     constexpr int RPB = WAVE ? 4 : 1;
+    constexpr int E = (int)sizeof(IO);
     __shared__ float lds[2][48];
     __shared__ float red[WAVE ? 4 : 1][WAVE ? 64 * K * V : 1];
     const int tid = WAVE ? threadIdx.x % 64 : threadIdx.x, nthr = WAVE ? 64 : blockDim.x;
-    const int wave = threadIdx.x / 64;
-    const int npack = a.columns / V, nscale = (a.columns + 127) / 128;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int nscale = (a.columns + 127) / 128, bytes = a.columns * E, dense = bytes;
     const float inv_n = 1.f / (float)a.columns;
     constexpr bool HOLD = K * V <= 8;
-    auto weight1 = [&](int p, int v) {
-        const int c = p * V + v;
-        return (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
-    };
-    auto weight2 = [&](int p, int v) { return a.pre ? a.pre[p * V + v] : 1.f; };
-    float w1[HOLD ? K : 1][HOLD ? V : 1], w2[HOLD ? K : 1][HOLD ? V : 1], dm[K][V], dp[K][V];
+    float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V], dm[K][V], dp[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int p = min(pack_at<V>(k, tid, nthr), npack - 1);
+        if constexpr (HOLD) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if constexpr (HOLD) {
-                w1[k][v] = weight1(p, v);
-                w2[k][v] = weight2(p, v);
-            }
-            dm[k][v] = dp[k][v] = 0.f;
-        }
+        for (int v = 0; v < V; ++v) dm[k][v] = dp[k][v] = 0.f;
     }
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? wave : 0);
-    Pack<IO, V> yr[K], gr[K], xr[CKPT ? 1 : K], sr[CKPT ? 1 : K], zr[CKPT ? 1 : K];
+    R yr[K], gr[K], xr[CKPT ? 1 : K], sr[CKPT ? 1 : K], zr[CKPT ? 1 : K];
     Kept<V> xk[CKPT ? K : 1], sk[CKPT ? K : 1], zk[CKPT ? K : 1];
     auto load = [&](int64_t r) {
-        const char *yb = (const char *)a.dy + r * a.dys, *gb = (const char *)a.dresidual_out + r * a.drs;
-        const char *xb = (const char *)a.x + r * a.xs, *sb = (const char *)a.residual + r * a.rs;
-        const char *zb = (const char *)a.z + r * a.zs;
-        const int64_t at = r * a.columns, sc = r * nscale;
+        const __amdgpu_buffer_rsrc_t yb = row_of(a.dy, r, a.dys, bytes);
+        const __amdgpu_buffer_rsrc_t gb = row_of(a.dresidual_out, r, a.drs, a.dresidual_out ? bytes : 0);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                const int64_t off = p * (V * (int)sizeof(IO));
-                yr[k] = load_pack<IO, V>(yb + off);
-                if (a.dresidual_out) gr[k] = load_pack<IO, V>(gb + off);
-                if constexpr (CKPT) {
-                    xk[k] = load_kept<V>(a.xq + at, a.xsc + sc, p);
-                    sk[k] = load_kept<V>(a.sq + at, a.ssc + sc, p);
-                    if (GATE) zk[k] = load_kept<V>(a.zq + at, a.zsc + sc, p);
-                } else {
-                    xr[k] = load_pack<IO, V>(xb + off);
-                    sr[k] = load_pack<IO, V>(sb + off);
-                    if (GATE) zr[k] = load_pack<IO, V>(zb + off);
-                }
-            }
+            const uint32_t at = (uint32_t)(pack_at<V>(k, tid, nthr) * (V * E));
+            yr[k] = buffer_load<R>(yb, at, 0);
+            gr[k] = buffer_load<R>(gb, at, 0);
+        }
+        if constexpr (CKPT) {
+            auto kept = [&](Kept<V> (&to)[K], const uint8_t *q, const float *sc) {
+                const __amdgpu_buffer_rsrc_t qb = row_of(q, r, a.columns, a.columns);
+                const __amdgpu_buffer_rsrc_t cb = row_of(sc, r, nscale * 4, nscale * 4);
+#pragma unroll
+                for (int k = 0; k < K; ++k) to[k] = load_kept<V>(qb, cb, pack_at<V>(k, tid, nthr));
+            };
+            kept(xk, a.xq, a.xsc);
+            kept(sk, a.sq, a.ssc);
+            if (GATE) kept(zk, a.zq, a.zsc);
+        } else {
+            auto whole = [&](R (&to)[K], const void *p, int64_t stride) {
+                const __amdgpu_buffer_rsrc_t pb = row_of(p, r, stride, bytes);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    to[k] = buffer_load<R>(pb, (uint32_t)(pack_at<V>(k, tid, nthr) * (V * E)), 0);
+            };
+            whole(xr, a.x, a.xs);
+            whole(sr, a.residual, a.rs);
+            if (GATE) whole(zr, a.z, a.zs);
         }
     };
     auto value = [&](const auto &raw, const auto &kept, int k, float (&f)[V]) {
@@ -297,7 +304,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
             kept_values<V>(kept[k], f);
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = (float)raw[k].v[v];
+            for (int v = 0; v < V; ++v) f[v] = RW::at(raw[k], v);
         }
     };
     if (row < a.rows) load(row);
@@ -306,20 +313,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
         float n1[K][V], h[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                float s[V];
-                value(xr, xk, k, n1[k]);
-                value(sr, sk, k, s);
+            if constexpr (!HOLD) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[0], w2[0]);
+            float s[V];
+            value(xr, xk, k, n1[k]);
+            value(sr, sk, k, s);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float w;
-                    if constexpr (HOLD) w = w2[k][v];
-                    else w = weight2(p, v);
-                    sums[0] = fmaf(n1[k][v], n1[k][v], sums[0]);
-                    sums[1] = fmaf(s[v], s[v], sums[1]);
-                    sums[2] = fmaf(w * (float)yr[k].v[v], s[v], sums[2]);
-                }
+            for (int v = 0; v < V; ++v) {
+                sums[0] = fmaf(n1[k][v], n1[k][v], sums[0]);
+                sums[1] = fmaf(s[v], s[v], sums[1]);
+                sums[2] = fmaf(w2[HOLD ? k : 0][v] * RW::at(yr[k], v), s[v], sums[2]);
             }
         }
         row_sums<WAVE, 3>(sums, lds[0]);
@@ -327,56 +329,45 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
         const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sums[1], inv_n, a.eps));
         const float mean2 = sums[2] * rstd2 * inv_n;   // of g n2
         float sum[1] = {0.f};
+        const __amdgpu_buffer_rsrc_t rb = row_of(a.dresidual, row, dense, bytes), zb = row_of(a.dz, row, dense, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                float s[V], z[V], dr[V], dz[V];
-                value(sr, sk, k, s);
-                if (GATE) value(zr, zk, k, z);
+            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
+            float s[V], z[V], dr[V], dz[V];
+            value(sr, sk, k, s);
+            if (GATE) value(zr, zk, k, z);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float c, w;
-                    if constexpr (HOLD) {
-                        c = w1[k][v];
-                        w = w2[k][v];
-                    } else {
-                        c = weight1(p, v);
-                        w = weight2(p, v);
-                    }
-                    const float dy = (float)yr[k].v[v], n2 = s[v] * rstd2;
-                    dp[k][v] = fmaf(dy, n2, dp[k][v]);
-                    float ds = rstd2 * fmaf(-n2, mean2, w * dy);
-                    if (a.dresidual_out) ds += (float)gr[k].v[v];
-                    dr[v] = a.alpha * ds;
-                    n1[k][v] *= rstd1;
-                    float t = ds;
-                    if (GATE) {
-                        const float sig = sigmoid_f32(z[v]);
-                        dz[v] = ds * c * n1[k][v] * (sig * fmaf(z[v], 1.f - sig, 1.f));
-                        t = ds * (z[v] * sig);
-                    }
-                    dm[k][v] = fmaf(t, n1[k][v], dm[k][v]);
-                    h[k][v] = t * c;
-                    sum[0] = fmaf(h[k][v], n1[k][v], sum[0]);
+            for (int v = 0; v < V; ++v) {
+                const float c = w1[HOLD ? k : 0][v], w = w2[HOLD ? k : 0][v];
+                const float dy = RW::at(yr[k], v), n2 = s[v] * rstd2;
+                dp[k][v] = fmaf(dy, n2, dp[k][v]);
+                const float ds = fmaf(rstd2, fmaf(-n2, mean2, w * dy), RW::at(gr[k], v));
+                dr[v] = a.alpha * ds;
+                n1[k][v] *= rstd1;
+                float t = ds;
+                if (GATE) {
+                    const float sig = sigmoid_f32(z[v]);
+                    dz[v] = ds * c * n1[k][v] * (sig * fmaf(z[v], 1.f - sig, 1.f));
+                    t = ds * (z[v] * sig);
                 }
-                const int64_t at = row * a.columns + p * V;
-                store_pack<IO, V>((IO *)a.dresidual + at, dr);
-                if (GATE) store_pack<IO, V>((IO *)a.dz + at, dz);
+                dm[k][v] = fmaf(t, n1[k][v], dm[k][v]);
+                h[k][v] = t * c;
+                sum[0] = fmaf(h[k][v], n1[k][v], sum[0]);
             }
+            buffer_store<IO, V>(rb, (uint32_t)(p * (V * E)), 0, dr);
+            if (GATE) buffer_store<IO, V>(zb, (uint32_t)(p * (V * E)), 0, dz);
         }
-        if (row + step < a.rows) load(row + step);
+        load(min(row + step, a.rows - 1));
         row_sums<WAVE, 1>(sum, lds[1]);
         const float mean1 = sum[0] * inv_n;
+        const __amdgpu_buffer_rsrc_t xb = row_of(a.dx, row, dense, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
-                float dx[V];
+            float dx[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) dx[v] = rstd1 * fmaf(-n1[k][v], mean1, h[k][v]);
-                store_pack<IO, V>((IO *)a.dx + row * a.columns + p * V, dx);
-            }
+            for (int v = 0; v < V; ++v) dx[v] = rstd1 * fmaf(-n1[k][v], mean1, h[k][v]);
+            buffer_store<IO, V>(xb, (uint32_t)(pack_at<V>(k, tid, nthr) * (V * E)), 0, dx);
         }
     }
     if (!a.part) return;
@@ -398,13 +389,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if (p < npack) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < V; ++v)
+                if (p * V < a.columns) {
                     out[p * V + v] = dm[k][v];
                     out[a.columns + p * V + v] = dp[k][v];
                 }
-            }
         }
     }
 }
