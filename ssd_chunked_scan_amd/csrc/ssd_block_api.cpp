@@ -34,16 +34,23 @@ ssd_status_t check_block(const ssd_block_shape_t *s, ssd_dtype_t io) {
     return check_reserved(s->reserved);
 }
 
-// Workgroups of the backward kernel, each one part of the column sums: about
-// 8192 columns in flight for each compute unit, which is what its registers
-// hold, and at most one a row.
-int block_parts(const ssd_block_shape_t *s, hipStream_t stream) {
-    const int64_t each = std::max<int64_t>(1, std::min<int64_t>(8, 8192 / s->columns));
-    return (int)std::min<int64_t>(each * ssd::compute_units(stream), s->rows);
+// Workgroups of the backward kernel, each one part of the column sums: twelve
+// waves for each compute unit, and at most one workgroup a row.  More rows at
+// once hide more latency but leave more parts to sum (16384 x 2560: 142 us with
+// 2 workgroups of 5 waves for each compute unit, 158 with 3, 168 with 1; 8192 x
+// 5120: 145 with 1 of 10, 158 with 2; 30000 x 1003: 107 with 3 of 4, 124 with
+// 2, 116 with 4).  `wide`: 16-byte accesses, eight columns a thread, else four
+// or, past 4096 columns, sixteen.
+int block_parts(const ssd_block_shape_t *s, bool wide, hipStream_t stream) {
+    const int64_t per = wide ? 8 : s->columns <= 4096 ? 4 : 16;
+    const int64_t waves = s->columns <= (wide ? 512 : 256) ? 4 : (s->columns + 64 * per - 1) / (64 * per);
+    return (int)std::min<int64_t>(std::max<int64_t>(1, 12 / waves) * ssd::compute_units(stream), s->rows);
 }
 
+// For either access, which the buffers' alignment decides.
 size_t block_bwd_bytes(const ssd_block_shape_t *s, hipStream_t stream) {
-    return round_up(sizeof(float) * 2 * (size_t)block_parts(s, stream) * s->columns, 256);
+    const int parts = std::max(block_parts(s, true, stream), block_parts(s, false, stream));
+    return round_up(sizeof(float) * 2 * (size_t)parts * s->columns, 256);
 }
 
 ssd::BlockArgs block_args(const ssd_block_shape_t *s, ssd_dtype_t io, const void *x, const void *z, const void *residual,
@@ -234,13 +241,13 @@ ssd_status_t ssd_block_norm_bwd(const ssd_block_shape_t *shape, ssd_dtype_t io, 
     a.dpre = dpre_weight;
     a.dscale = dscale;
     a.part = sums ? (float *)workspace : nullptr;
-    a.parts = block_parts(shape, (hipStream_t)stream);
     if (checkpoint) use_checkpoint(a, checkpoint);
     const int n = wide_of(io);
     const int64_t dense = shape->columns * (int64_t)e;
     const bool wide = Access(shape->columns % n == 0 && checkpoint_aligned(checkpoint, n), n, io).in(x, a.xs).in(z, a.zs)
                           .in(residual_out, a.rs).in(dy, a.dys).in(dresidual_out, a.drs).in(dx, dense)
                           .in(dresidual, dense).in(dz, dense).ok;
+    a.parts = block_parts(shape, wide, (hipStream_t)stream);
     (void)hipGetLastError();   // not an earlier call's
     ssd::launch_block_bwd(io == SSD_BF16, wide, a, (hipStream_t)stream);
     return launched("ssd_block_norm_bwd");

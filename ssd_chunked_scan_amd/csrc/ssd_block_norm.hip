@@ -399,13 +399,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
     }
 }
 
-// Sums the parts in a fixed order: 64 columns of one plane a workgroup, 16
+// Sums the parts in a fixed order: 32 columns of one plane a workgroup, 32
 // threads a column over runs of parts, joined in order.
+constexpr int kFinish = 32;
+
 __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x % 64, run = threadIdx.x / 64, n = a.columns;
-    const int ncol = (n + 63) / 64, plane = blockIdx.x / ncol, c = blockIdx.x % ncol * 64 + lane;
-    const int per = (a.parts + 15) / 16, k0 = min(run * per, a.parts), k1 = min(k0 + per, a.parts);
+    __shared__ float s[kFinish][kFinish + 1];
+    const int lane = threadIdx.x % kFinish, run = threadIdx.x / kFinish, n = a.columns;
+    const int ncol = (n + kFinish - 1) / kFinish, plane = blockIdx.x / ncol, c = blockIdx.x % ncol * kFinish + lane;
+    const int per = (a.parts + kFinish - 1) / kFinish, k0 = min(run * per, a.parts), k1 = min(k0 + per, a.parts);
     const float *p = a.part + (int64_t)plane * n + min(c, n - 1);
     float acc = 0.f;
 #pragma unroll 8
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
     s[run][lane] = acc;
     __syncthreads();
     if (run == 0 && c < n) {
-        for (int r = 1; r < 16; ++r) acc += s[r][lane];
+        for (int r = 1; r < kFinish; ++r) acc += s[r][lane];
         if (plane == 1) {
             if (a.dpre) a.dpre[c] = acc;
         } else {
@@ -425,8 +427,12 @@ __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
 
 template <typename IO, int V, bool WAVE, int K>
 static void block_fwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
+    // as many workgroups as are resident: 28 waves a compute unit with
+    // checkpoints, whose registers leave room for no more (16384 x 2560: 126 us,
+    // 136 with 32), 32 without
     const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
-    const dim3 grid((unsigned)std::min(rows, std::max<int64_t>(1, (int64_t)a.cus * (2048 / nthr))));
+    const int64_t fit = (int64_t)a.cus * std::max(1, (a.xq ? 28 : 32) / (nthr / 64));
+    const dim3 grid((unsigned)std::min(rows, fit));
 #define SSD_BLOCK_FWD(G, C)                                                                                  \
     if (!a.z == !G && !a.xq == !C)                                                                           \
         hipLaunchKernelGGL((block_fwd_kernel<IO, V, WAVE, K, G, C>), grid, dim3(nthr), 0, stream, a);
@@ -479,7 +485,7 @@ void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t s
         wide ? block_bwd_shape<bf16, 8, 1, 1, 2>(a, stream) : block_bwd_shape<bf16, 1, 4, 4, 16>(a, stream);
     else
         wide ? block_bwd_shape<float, 4, 2, 2, 4>(a, stream) : block_bwd_shape<float, 1, 4, 4, 16>(a, stream);
-    if (a.part) hipLaunchKernelGGL(block_finish_kernel, dim3((a.columns + 63) / 64 * 2), dim3(1024), 0, stream, a);
+    if (a.part) hipLaunchKernelGGL(block_finish_kernel, dim3((a.columns + kFinish - 1) / kFinish * 2), dim3(1024), 0, stream, a);
 }
 
 }  // namespace ssd
