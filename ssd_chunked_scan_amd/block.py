@@ -9,7 +9,7 @@ from typing import Tuple
 
 import ssd_chunked_scan_amd as ssd
 from . import layer
-from .layer import _dense, _io, _like, _On, _output, _outputs, _ptr, _tokens, _workspace
+from .layer import _dense, _io, _like, _On, _outputs, _ptr, _tokens, _workspace
 
 _I64, _VP = ctypes.c_int64, ctypes.c_void_p
 
@@ -105,7 +105,8 @@ def ssd_block_norm_fwd(x, residual, post_weight=None, pre_weight=None, z=None, s
     [..., ceil(D / 128)]); z's only with z."""
     lib = layer._library()
     io, shape = _block_common("ssd_block_norm_fwd", x, z, post_weight, pre_weight, scale, alpha, eps)
-    shape.x_stride = _tokens(x, "x", x.shape, x.dtype, x.device)
+    if not x.is_contiguous():
+        shape.x_stride = _tokens(x, "x", x.shape, x.dtype, x.device)
     shape.residual_stride = _tokens(residual, "residual", x.shape, x.dtype, x.device)
     with _On(x.device, stream) as st:
         y = _like(y, "y", x)
@@ -135,7 +136,8 @@ def ssd_block_norm_bwd(x, residual_out, post_weight, pre_weight, dy, z=None, sca
     name = "ssd_block_norm_bwd"
     io, shape = _block_common(name, dy, z, post_weight, pre_weight, scale, alpha, eps)
     dev, dt = dy.device, dy.dtype
-    shape.dy_stride = _tokens(dy, "dy", dy.shape, dt, dev)
+    if not dy.is_contiguous():
+        shape.dy_stride = _tokens(dy, "dy", dy.shape, dt, dev)
     struct, gate = None, z is not None
     if checkpoint is not None:
         if x is not None or residual_out is not None or z is not None:
@@ -177,17 +179,18 @@ def _mx4_rows(name, x):
 
 def _mx4_operand(q, scales, name, scales_name, device):
     """Checks codes and scales; the rows and the padded columns they hold."""
-    torch = layer.torch
-    if q.dim() < 1 or q.shape[-1] % 64 != 0 or q.shape[-1] == 0:
+    u8 = layer.torch.uint8
+    half = q.shape[-1] if q.dim() else 0
+    if half == 0 or half % 64 != 0:
         raise ValueError(f"{name}: expected [..., columns / 2], columns padded to a multiple of 128, got {tuple(q.shape)}")
-    rows, half = _mx4_rows(name, q)
-    _dense(q, name, q.shape, torch.uint8, device)
-    _dense(scales, scales_name, (half // 64, rows, 4), torch.uint8, device)
+    rows = q.numel() // half
+    _dense(q, name, q.shape, u8, device)
+    _dense(scales, scales_name, (half // 64, rows, 4), u8, device)
     return rows, 2 * half
 
 
 def _mx4_device(name, q):
-    if q.device.type != "cuda":
+    if not q.is_cuda:
         raise ValueError(f"{name} runs on the GPU only (on {q.device})")
     return q.device
 
@@ -198,6 +201,14 @@ def _mx4_io(name, dtype) -> int:
     if dtype is layer.torch.float32:
         return 0
     raise TypeError(f"{name}: dtype must be bfloat16 or float32, got {dtype}")
+
+
+def _mx4_output(given, name, like, shape, dtype):
+    """An output on like's device."""
+    if given is None:
+        return like.new_empty(shape, dtype=dtype)
+    _dense(given, name, shape, dtype, like.device)
+    return given
 
 
 def ssd_mx4_quant(x, q=None, scales=None, stream=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
@@ -211,10 +222,10 @@ def ssd_mx4_quant(x, q=None, scales=None, stream=None) -> Tuple["torch.Tensor", 
     rows, K = _mx4_rows("ssd_mx4_quant", x)
     dev, u8 = x.device, layer.torch.uint8
     kb = -(-K // 128)
-    shape = Mx4Shape(rows, K, 0, _tokens(x, "x", x.shape, x.dtype, dev))
+    shape = Mx4Shape(rows, K, 0, 0 if x.is_contiguous() else _tokens(x, "x", x.shape, x.dtype, dev))
     with _On(dev, stream) as st:
-        q = _output(q, "q", (*x.shape[:-1], 64 * kb), u8, dev)
-        scales = _output(scales, "scales", (kb, rows, 4), u8, dev)
+        q = _mx4_output(q, "q", x, (*x.shape[:-1], 64 * kb), u8)
+        scales = _mx4_output(scales, "scales", x, (kb, rows, 4), u8)
         status = lib.ssd_mx4_quant(ctypes.byref(shape), io, x.data_ptr(), q.data_ptr(), scales.data_ptr(), st)
     ssd._check(status)
     return q, scales
@@ -233,7 +244,7 @@ def ssd_mx4_dequant(q, scales, columns: int, dtype=None, y=None, stream=None) ->
         raise ValueError(f"{name}: columns {columns} does not match codes of {kp} padded columns")
     shape = Mx4Shape(rows, columns, 0, 0)
     with _On(dev, stream) as st:
-        y = _output(y, "y", (*q.shape[:-1], columns), dtype, dev)
+        y = _mx4_output(y, "y", q, (*q.shape[:-1], columns), dtype)
         status = lib.ssd_mx4_dequant(ctypes.byref(shape), io, q.data_ptr(), scales.data_ptr(), y.data_ptr(), st)
     ssd._check(status)
     return y
@@ -243,7 +254,8 @@ def _mx4_weights(name, wq, wscales, bias, dev):
     if wq.dim() != 2:
         raise ValueError(f"{name}: wq must be [N, columns / 2], got {tuple(wq.shape)}")
     N, kp = _mx4_operand(wq, wscales, "wq", "wscales", dev)
-    _dense(bias, "bias", (N,), layer.torch.float32, dev)
+    if bias is not None:
+        _dense(bias, "bias", (N,), layer.torch.float32, dev)
     return N, kp
 
 
@@ -262,7 +274,7 @@ def ssd_mx4_matmul(q, scales, wq, wscales, bias=None, dtype=None, y=None, stream
         raise ValueError(f"{name}: q has {kp} padded columns, wq {wkp}")
     shape = Mx4Shape(rows, kp, N, 0)
     with _On(dev, stream) as st:
-        y = _output(y, "y", (*q.shape[:-1], N), dtype, dev)
+        y = _mx4_output(y, "y", q, (*q.shape[:-1], N), dtype)
         status = lib.ssd_mx4_matmul(ctypes.byref(shape), io, q.data_ptr(), scales.data_ptr(), wq.data_ptr(),
                                     wscales.data_ptr(), _ptr(bias), y.data_ptr(), st)
     ssd._check(status)
@@ -281,9 +293,9 @@ def ssd_mx4_linear(x, wq, wscales, bias=None, y=None, workspace=None, stream=Non
     N, kp = _mx4_weights(name, wq, wscales, bias, dev)
     if not kp - 128 < K <= kp:
         raise ValueError(f"{name}: x has {K} columns, wq {kp} padded ones")
-    shape = Mx4Shape(rows, K, N, _tokens(x, "x", x.shape, x.dtype, dev))
+    shape = Mx4Shape(rows, K, N, 0 if x.is_contiguous() else _tokens(x, "x", x.shape, x.dtype, dev))
     with _On(dev, stream) as st:
-        y = _output(y, "y", (*x.shape[:-1], N), x.dtype, dev)
+        y = _mx4_output(y, "y", x, (*x.shape[:-1], N), x.dtype)
         ws = _workspace(workspace, int(lib.ssd_mx4_linear_workspace_bytes(ctypes.byref(shape), io)), dev)
         status = lib.ssd_mx4_linear(ctypes.byref(shape), io, x.data_ptr(), wq.data_ptr(), wscales.data_ptr(), _ptr(bias),
                                     y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), st)

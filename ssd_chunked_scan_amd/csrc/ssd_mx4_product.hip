@@ -22,15 +22,6 @@ namespace ssd {
 
 constexpr int kFewWaves = 8;
 
-template <typename IN>
-struct Mx4Tokens {
-    static constexpr bool kQuantised = false;
-};
-template <>
-struct Mx4Tokens<uint8_t> {
-    static constexpr bool kQuantised = true;
-};
-
 template <typename OUT>
 __device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, const float (&v)[4], bool wide) {
     OUT *y = (OUT *)a.y + t * a.n + n;
@@ -48,7 +39,9 @@ __device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, con
 
 template <typename IN, typename OUT, int MT, int NT, bool WIDE>
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs a) {
-    constexpr bool PRE = Mx4Tokens<IN>::kQuantised;
+    constexpr bool PRE = std::is_same_v<IN, uint8_t>;   // the activations come in 4 bits
+    static_assert(PRE || MT == 1, "quantised on the way: up to 16 tokens");
+    typedef std::conditional_t<PRE, float, IN> X;
     __shared__ float red[kFewWaves][NT * MT][64][4];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int r = lane % 16, g = lane / 16;
@@ -63,41 +56,52 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs 
         wp[j] = a.w + n * a.kblocks * 64 + g * 16;
         wsp[j] = (const uint8_t *)a.ws + n * 4 + g;
     }
-    for (int kb = wave; kb < a.kblocks; kb += kFewWaves) {
-        i32x4 w[NT], t[MT];
-        int ws[NT], ts[MT];
+    // two blocks' loads at a time
+    for (int kb0 = wave; kb0 < a.kblocks; kb0 += 2 * kFewWaves) {
+        i32x4 w[2][NT], t[2][MT];
+        int ws[2][NT], ts[2][MT];
+        Pack<X, 8> v[2][PRE ? 1 : 4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            w[j] = *(const i32x4 *)(wp[j] + kb * 64);
-            ws[j] = wsp[j][(int64_t)kb * a.n * 4];
-        }
+        for (int u = 0; u < 2; ++u) {
+            const int kb = kb0 + u * kFewWaves;
+            if (kb >= a.kblocks) break;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int tok = min(i * 16 + r, m - 1);
+            for (int j = 0; j < NT; ++j) {
+                w[u][j] = *(const i32x4 *)(wp[j] + kb * 64);
+                ws[u][j] = wsp[j][(int64_t)kb * a.n * 4];
+            }
             if constexpr (PRE) {
-                t[i] = *(const i32x4 *)(a.a + ((int64_t)tok * a.kblocks + kb) * 64 + g * 16);
-                ts[i] = ((const uint8_t *)a.as)[((int64_t)kb * m + tok) * 4 + g];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int tok = min(i * 16 + r, m - 1);
+                    t[u][i] = *(const i32x4 *)(a.a + ((int64_t)tok * a.kblocks + kb) * 64 + g * 16);
+                    ts[u][i] = ((const uint8_t *)a.as)[((int64_t)kb * m + tok) * 4 + g];
+                }
             } else {
-                const char *row = (const char *)a.x + tok * a.xs;
-                Pack<IN, 8> v[4];
-                uint32_t most = 0;
+                const char *row = (const char *)a.x + min(r, m - 1) * a.xs;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = mx4_load8<IN, WIDE>(row, kb * 128 + g * 32 + q * 8, a.columns);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) most = max(most, mx4_most<IN>(v[q]));
-                const uint32_t byte = mx4_scale_byte(most);
-                const float scale = mx4_scale(byte);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) t[i][q] = (int)mx4_codes<IN>(v[q], scale);
-                ts[i] = (int)byte;
+                for (int q = 0; q < 4; ++q) v[u][q] = mx4_load8<X, WIDE>(row, kb * 128 + g * 32 + q * 8, a.columns);
             }
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int u = 0; u < 2; ++u) {
+            if (kb0 + u * kFewWaves >= a.kblocks) break;
+            if constexpr (!PRE) {
+                uint32_t most = 0;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_operand(w[j]), mx4_operand(t[i]), acc[j][i],
-                                                                             4, 4, 0, ws[j], 0, ts[i]);
+                for (int q = 0; q < 4; ++q) most = max(most, mx4_most<X>(v[u][q]));
+                const uint32_t byte = mx4_scale_byte(most);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) t[u][0][q] = (int)mx4_codes<X>(v[u][q], mx4_scale(byte));
+                ts[u][0] = (int)byte;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_operand(w[u][j]), mx4_operand(t[u][i]),
+                                                                                 acc[j][i], 4, 4, 0, ws[u][j], 0, ts[u][i]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -523,12 +527,18 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
 
 template <typename IN, typename OUT, int MT, bool WIDE>
 static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
-    // Two tiles of 16 outputs share a workgroup's activations where that still
-    // gives every compute unit one.
-    if ((a.n + 31) / 32 >= a.cus)
-        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, 2, WIDE>), dim3((a.n + 31) / 32), dim3(64 * kFewWaves), 0, stream, a);
-    else
-        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, 1, WIDE>), dim3((a.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, a);
+    // Up to four tiles of 16 outputs share a workgroup's activations where that
+    // leaves 5/8 of the compute units one: 1 x 10576 x 2560 7.2 us with four, 7.6
+    // with two, 9.4 with one; 8 x 2560 x 5120 10.9, 8.6 and 7.8.
+    const auto fits = [&](int nt) { return 8 * (int64_t)((a.n + 16 * nt - 1) / (16 * nt)) >= 5 * (int64_t)a.cus; };
+    const auto launch = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, WIDE>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * kFewWaves), 0,
+                           stream, a);
+    };
+    if (fits(4)) launch(std::integral_constant<int, 4>{});
+    else if (fits(2)) launch(std::integral_constant<int, 2>{});
+    else launch(std::integral_constant<int, 1>{});
 }
 
 template <typename OUT>

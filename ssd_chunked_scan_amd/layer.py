@@ -56,7 +56,7 @@ def declare(lib) -> None:
 
 
 def _io(x, name: str) -> int:
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} runs on the GPU only (x is on {x.device})")
     if x.dtype is torch.bfloat16:
         return 1
@@ -115,15 +115,16 @@ def _ptr(t):
 
 
 # The current stream's handle of a device, without the Stream object around it
-# (2 us of a 10 us call) where torch offers that.
-_raw_stream = None
+# (2 us of a 10 us call), and the current device, where torch offers that.
+_raw_stream = _current_device = None
 
 
 def _library():
     """libssd.so, and torch with the first call."""
-    global torch, _raw_stream
+    global torch, _raw_stream, _current_device
     if torch is None:
         import torch as module
+        _current_device = getattr(module._C, "_cuda_getDevice", module.cuda.current_device)
         _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: module.cuda.current_stream(index).cuda_stream)
         torch = module
@@ -138,7 +139,7 @@ class _On:
 
     def __init__(self, device, stream):
         self.index, self.stream = device.index, stream
-        self.stack = None if stream is None and device.index == torch.cuda.current_device() else contextlib.ExitStack()
+        self.stack = None if stream is None and device.index == _current_device() else contextlib.ExitStack()
 
     def __enter__(self):
         if self.stack is not None:
