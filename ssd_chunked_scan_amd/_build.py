@@ -92,6 +92,9 @@ def _parse_functions(asm_text: str):
         if "ssd lookahead wait" in raw and cur is not None:
             cur.append(("mark", "ssd lookahead wait"))   # see vmem_lds_sync_lookahead
             continue
+        if "ssd ring wait" in raw and cur is not None:
+            cur.append(("mark", "ssd ring wait"))        # see vmem_lds_sync_ring
+            continue
         if "ssd touch wait" in raw and cur is not None:
             cur.append(("mark", "ssd touch wait"))       # see vmem_lds_sync_touch
             continue
@@ -188,6 +191,38 @@ _WAIT_VM = re.compile(r"s_waitcnt\s+vmcnt\((\d+)\)")
 VMCNT_MAX = 63
 
 
+def _check_ring_wait(items, i: int, need: int, what: str) -> None:
+    """From the wait at items[i], along every path backwards, `need` direct-to-LDS
+    loads must come before any other vector-memory operation and before the
+    function's start."""
+    sources = {}
+    for k, (kind, text) in enumerate(items):
+        if kind == "ins" and text.startswith(("s_branch", "s_cbranch")):
+            sources.setdefault(text.split()[-1], []).append(k)
+    stack, seen = [(i - 1, need)], set()
+    while stack:
+        j, left = stack.pop()
+        while left > 0:
+            if j < 0:
+                raise RuntimeError(f"{what} reaches the function's start {left} direct-to-LDS loads short")
+            if (j, left) in seen:
+                break
+            seen.add((j, left))
+            kind, t = items[j]
+            if kind == "label":
+                stack += [(k, left) for k in sources.get(t, ())]
+            elif kind == "ins":
+                if _loads_to_lds(t):
+                    left -= 1
+                elif t.startswith(_VMEM):
+                    raise RuntimeError(f"{what} would leave an ordinary vector-memory operation in flight: {t}")
+            # from a label to what precedes it, unless that leaves for elsewhere
+            if kind == "label" and j > 0 and items[j - 1][0] == "ins" and \
+                    items[j - 1][1].startswith(("s_branch", "s_setpc", "s_endpgm")):
+                break
+            j -= 1
+
+
 def check_counted_barrier_waits(asm_text: str, where: str) -> int:
     """A barrier whose wait leaves K > 0 vector-memory operations in flight is
     only correct if the K most recent ones are not direct-to-LDS loads (whose
@@ -213,6 +248,9 @@ def check_counted_barrier_waits(asm_text: str, where: str) -> int:
             # before the wait, with no label or vector-memory operation in
             # between
             marked, touch, q = False, False, i - 1
+            if any(items[k] == ("mark", "ssd ring wait") for k in range(max(0, i - 3), i)):
+                _check_ring_wait(items, i, need, f"{where}: {fname}: ring wait '{text}'")
+                continue
             while q >= 0 and items[q][0] != "label":
                 if items[q][0] == "mark" and items[q][1] in ("ssd lookahead wait", "ssd touch wait"):
                     marked = True

@@ -10,7 +10,7 @@ void launch_block_fwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t s
 void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream);
 void launch_mx4_quant(bool bf16_io, bool wide, const Mx4QuantArgs &a, hipStream_t stream);
 void launch_mx4_dequant(bool bf16_io, bool wide, const Mx4QuantArgs &a, hipStream_t stream);
-void launch_mx4_product(bool bf16_out, bool wide, bool few, const Mx4ProductArgs &a, hipStream_t stream);
+void launch_mx4_product(bool bf16_out, bool wide, const Mx4ProductArgs &a, hipStream_t stream);
 }  // namespace ssd
 
 namespace {
@@ -100,8 +100,7 @@ bool checkpoint_aligned(const ssd_block_checkpoint_t *c, int n) {
 
 // --------------------------------------------------------- 4-bit operands
 
-constexpr int64_t kFewTokens = 32;     // one or two matrix instructions of 16 tokens a wave
-constexpr int64_t kFewQuantised = 16;  // the few-token kernel quantises by itself up to here
+constexpr int64_t kFewQuantised = 16;   // tokens that the product's kernel quantises by itself
 
 int64_t kblocks_of(const ssd_mx4_shape_t *s) { return (s->columns + 127) / 128; }
 
@@ -295,7 +294,7 @@ ssd_status_t ssd_mx4_matmul(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const 
     a.a = (const uint8_t *)q;
     a.as = (const uint32_t *)scales;
     (void)hipGetLastError();   // not an earlier call's
-    ssd::launch_mx4_product(io == SSD_BF16, true, a.m <= kFewTokens, a, (hipStream_t)stream);
+    ssd::launch_mx4_product(io == SSD_BF16, true, a, (hipStream_t)stream);
     return launched("ssd_mx4_matmul");
 }
 
@@ -320,14 +319,14 @@ ssd_status_t ssd_mx4_linear(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const 
     if (bytes == 0) {
         a.x = x;
         a.xs = qa.xs;
-        ssd::launch_mx4_product(io == SSD_BF16, quant_wide(qa), true, a, (hipStream_t)stream);
+        ssd::launch_mx4_product(io == SSD_BF16, quant_wide(qa), a, (hipStream_t)stream);
     } else {
         qa.q = (uint8_t *)workspace;
         qa.scales = (uint32_t *)((char *)workspace + linear_codes(shape));
         ssd::launch_mx4_quant(io == SSD_BF16, quant_wide(qa), qa, (hipStream_t)stream);
         a.a = qa.q;
         a.as = qa.scales;
-        ssd::launch_mx4_product(io == SSD_BF16, true, a.m <= kFewTokens, a, (hipStream_t)stream);
+        ssd::launch_mx4_product(io == SSD_BF16, true, a, (hipStream_t)stream);
     }
     return launched("ssd_mx4_linear");
 }

@@ -213,57 +213,74 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const Mx4ProductArgs &a, int6
                    rows > 0 ? ((uint32_t)rows * (uint32_t)a.n - (uint32_t)n0) * (uint32_t)sizeof(OUT) : 0u);
 }
 
-// Up to 256 columns: one load of everything, one barrier.  A workgroup of four
-// waves owns 64 tokens x 64 outputs.  Bound by y.
+// Problems of few tiles, whose time is the latency of their loads: a workgroup of
+// four waves owns 64 tokens x 64 outputs, and kRing - 1 stages of 256 columns
+// are on their way while one is multiplied (512 x 1024 x 1536: 4.2 us, 5.4 with
+// one on its way; 128 x 2560 x 5120: 8.0 and 10.4).  An empty kernel takes 1.6.
+constexpr int kRing = 4;
+
 template <typename OUT>
-__global__ __launch_bounds__(256) void mx4_short_kernel(Mx4ProductArgs a, int tiles_n) {
-    constexpr int ROWS = 128, BLOCK = ROWS * 64 + ROWS * 4;   // of 128 columns: codes, scales
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * BLOCK];
+__global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int tiles_n) {
+    constexpr int ROWS = 128, CODES = ROWS * 128, STAGE = CODES + ROWS * 8, LOADS = 5;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * STAGE];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int id = xcd_contiguous(blockIdx.x, gridDim.x);
     const int64_t m0 = (int64_t)(id / tiles_n) * 64;
-    const int n0 = id % tiles_n * 64, pitch = a.kblocks * 64;
+    const int n0 = id % tiles_n * 64, pitch = a.kblocks * 64, last = (a.kblocks - 1) / 2;
     const int mleft = (int)min((int64_t)64, a.m - m0), nleft = min(64, a.n - n0);
     const __amdgpu_buffer_rsrc_t as = bounded(a.a + m0 * pitch, (uint32_t)mleft * (uint32_t)pitch);
     const __amdgpu_buffer_rsrc_t ws = bounded(a.w + (int64_t)n0 * pitch, (uint32_t)nleft * (uint32_t)pitch);
-    for (int kb = 0; kb < a.kblocks; ++kb) {
-        uint8_t *to = lds + kb * BLOCK;
+    const int lrow = wave * 8 + lane / 8;
+    const uint32_t code_at = (uint32_t)lrow * (uint32_t)pitch + ((lane % 8) ^ (lrow / 2 % 8)) * 16;
+    // 8 rows of codes four times, 64 words of scales once.  The second half of
+    // an odd last stage brings other codes and scale bytes of 0: products below
+    // 2^-240, which fp32 sums round away.
+    const bool tok = wave % 2 == 0;
+    const uint32_t *scales = tok ? a.as + m0 : a.ws + n0;
+    const int64_t scale_pitch = tok ? a.m : a.n;
+    const uint32_t scale_bytes = (uint32_t)(tok ? mleft : nleft) * 4u;
+    auto load = [&](int st, int buf) {
+        uint8_t *to = lds + buf * STAGE;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {   // 16 rows a load: tokens, weights
-            const int row = wave * 16 + lane / 4;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(i ? ws : as, (__attribute__((address_space(3))) void *)(to + (i * 4 + wave) * 1024),
-                                                     16, row * pitch + kb * 64 + ((lane % 4) ^ (row / 4 % 4)) * 16, 0, 0, 0);
-        }
-        if (wave < 2) {
-            const __amdgpu_buffer_rsrc_t sc = wave ? bounded(a.ws + (int64_t)kb * a.n + n0, nleft * 4u)
-                                                   : bounded(a.as + (int64_t)kb * a.m + m0, mleft * 4u);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(sc, (__attribute__((address_space(3))) void *)(to + ROWS * 64 + wave * 256), 4,
-                                                     lane * 4, 0, 0, 0);
-        }
-    }
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                i < 2 ? as : ws, (__attribute__((address_space(3))) void *)(to + (i * 4 + wave) * 1024), 16,
+                code_at + (uint32_t)(i % 2 * 32 * pitch + st * 128), 0, 0, 0);
+        const int kb = 2 * st + wave / 2;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(bounded(scales + kb * scale_pitch, kb < a.kblocks ? scale_bytes : 0u),
+                                                 (__attribute__((address_space(3))) void *)(to + CODES + wave * 256), 4,
+                                                 lane * 4, 0, 0, 0);
+    };
     const int wm = wave % 2, wn = wave / 2, r = lane % 32, g = lane / 32;
     f32x16 acc = {};
     if (a.bias) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] = a.bias[min(n0 + 32 * wn + 8 * (e / 4) + 4 * g + e % 4, a.n - 1)];
     }
-    vmem_lds_sync();
-    for (int kb = 0; kb < a.kblocks; ++kb) {
-        const uint8_t *at = lds + kb * BLOCK;
-        const int tr = wm * 32 + r, wr = 64 + wn * 32 + r;
-        // lanes 0 .. 31 take blocks 0 and 1 of the four, lanes 32 .. 63 the others
-        const int ts = (int)(*(const uint32_t *)(at + ROWS * 64 + tr * 4) >> (16 * g));
-        const int wsc = (int)(*(const uint32_t *)(at + ROWS * 64 + wr * 4) >> (16 * g));
-        i32x4 t[2], w[2];
+    // (past the end: the last stage again, which nothing reads)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            t[s] = *(const i32x4 *)(at + tr * 64 + ((2 * g + s) ^ (tr / 4 % 4)) * 16);
-            w[s] = *(const i32x4 *)(at + wr * 64 + ((2 * g + s) ^ (wr / 4 % 4)) * 16);
+    for (int i = 0; i < kRing - 1; ++i) load(min(i, last), i);
+    for (int st = 0, buf = 0; st <= last; ++st) {
+        vmem_lds_sync_ring<(kRing - 2) * LOADS>();
+        load(min(st + kRing - 1, last), buf == 0 ? kRing - 1 : buf - 1);
+        const uint8_t *at = lds + buf * STAGE;
+        // scales: [block][tokens, weights]
+        const int ts = *(const int *)(at + CODES + g * 512 + (wm * 32 + r) * 4);
+        const int wsc = *(const int *)(at + CODES + g * 512 + 256 + (wn * 32 + r) * 4);
+        i32x4 t[4], w[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int piece = ((4 * g + s) ^ (r / 2 % 8)) * 16;
+            t[s] = *(const i32x4 *)(at + (wm * 32 + r) * 128 + piece);
+            w[s] = *(const i32x4 *)(at + (64 + wn * 32 + r) * 128 + piece);
         }
         acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[0]), mx4_operand(t[0]), acc, 4, 4, 0, wsc, 0, ts);
         acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[1]), mx4_operand(t[1]), acc, 4, 4, 1, wsc, 1, ts);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[2]), mx4_operand(t[2]), acc, 4, 4, 2, wsc, 2, ts);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(w[3]), mx4_operand(t[3]), acc, 4, 4, 3, wsc, 3, ts);
+        buf = buf == kRing - 1 ? 0 : buf + 1;
     }
-    lds_sync();
+    vmem_lds_sync();
     typedef Mx4Chunk<OUT> CH;
     uint8_t *mine = lds + wave * kChunk;
     const __amdgpu_buffer_rsrc_t ys = rows_of_y<OUT>(a, m0, mleft, n0);
@@ -275,7 +292,7 @@ __global__ __launch_bounds__(256) void mx4_short_kernel(Mx4ProductArgs a, int ti
     }
 }
 
-// More columns: a workgroup owns BM tokens x BN outputs at a time and walks
+// Problems of many tiles: a workgroup owns BM tokens x BN outputs at a time and walks
 // them 256 columns a stage, then goes on to its next tile without a pause: one
 // stage is in LDS, the next one on its way.  What shapes it, measured for 16384 x
 // 10576 x 2560 (a 16384^3 bf16 product of the library reaches 1.6 PFLOP/s here):
@@ -558,26 +575,32 @@ static void mx4_tile_launch(const Mx4ProductArgs &a, hipStream_t stream) {
                        stream, a, tm, tn, 4);
 }
 
-// The largest tile that still occupies the device, in us for m x 2560 x 5120
-// and m x 10576 x 2560 with tiles of 256 / 128 / 64: m = 4096: 33 41 57 and 60 70
-// 117; 2048: 30 24 31 and 38 38 59; 1024: 28 16 19 and 22 23 34; 512: 46 15
-// 14 and 30 20 19; 256: 46 15 11 and 28 16 11.  So 256 from 5/8 of the compute
-// units on, 64 while one round of three a compute unit holds them all.
+// By tiles, in us with tiles of 256 / 128 / 64: m x 2560 x 5120, m = 4096: 33 41
+// 57; 2048: 30 24 34; 1024: 29 17 19; 512: 26 15 15; 256: 26 15 8; m x 10576 x
+// 2560, m = 4096: 60 70 117; 2048: 41 40 74; 1024: 23 24 40; 512: 18 15 23; 256:
+// 17 11 13; 128: 17 10 8; m x 4096 x 512, m = 2048: 11 9 12; 512: 9 6 4.  So 64
+// while two a compute unit hold them all, 256 from 5/8 of the compute units on.
 template <typename OUT>
 static void mx4_tile_out(const Mx4ProductArgs &a, hipStream_t stream) {
     const auto tiles = [&](int b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b); };
-    if (a.kblocks <= 2)
-        hipLaunchKernelGGL((mx4_short_kernel<OUT>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
+    if (a.kblocks <= 2 || tiles(64) <= 2 * (int64_t)a.cus)
+        hipLaunchKernelGGL((mx4_ring_kernel<OUT>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
     else if (8 * tiles(256) >= 5 * (int64_t)a.cus)
         mx4_tile_launch<OUT, 256, 256, 128, 64, 1>(a, stream);
-    else if (tiles(64) > 3 * (int64_t)a.cus)
-        mx4_tile_launch<OUT, 128, 128, 64, 64, 2>(a, stream);
     else
-        mx4_tile_launch<OUT, 64, 64, 32, 32, 3>(a, stream);
+        mx4_tile_launch<OUT, 128, 128, 64, 64, 2>(a, stream);
 }
 
-void launch_mx4_product(bool bf16_out, bool wide, bool few, const Mx4ProductArgs &a, hipStream_t stream) {
-    if (few)
+// Up to 16 tokens are quantised on the way or share the weights' reading with
+// nothing else; up to 32 go the same way where 64 outputs a workgroup would
+// leave half of the compute units idle (32 x 2560 x 5120: 6.7 us, 8.0 in tiles; 32 x
+// 10576 x 2560: 7.6 and 5.3).
+static bool mx4_few(const Mx4ProductArgs &a) {
+    return a.m <= 16 || (a.m <= 32 && (a.n + 63) / 64 <= a.cus / 2);
+}
+
+void launch_mx4_product(bool bf16_out, bool wide, const Mx4ProductArgs &a, hipStream_t stream) {
+    if (mx4_few(a))
         bf16_out ? mx4_few_out<bf16>(wide, a, stream) : mx4_few_out<float>(wide, a, stream);
     else
         bf16_out ? mx4_tile_out<bf16>(a, stream) : mx4_tile_out<float>(a, stream);

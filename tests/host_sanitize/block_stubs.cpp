@@ -104,9 +104,9 @@ void launch_mx4_dequant(bool bf16_io, bool, const Mx4QuantArgs &a, hipStream_t) 
     wr(a.y, (size_t)a.rows * a.columns * (bf16_io ? 2 : 4));
 }
 
-void launch_mx4_product(bool bf16_out, bool, bool few, const Mx4ProductArgs &a, hipStream_t) {
+void launch_mx4_product(bool bf16_out, bool, const Mx4ProductArgs &a, hipStream_t) {
     ++g_block_launches;
-    if (a.cus <= 0 || !a.x == !a.a || (a.x && a.m > 16) || (few && a.m > 64)) __builtin_trap();
+    if (a.cus <= 0 || !a.x == !a.a || (a.x && a.m > 16)) __builtin_trap();
     if (a.x) {
         rd_rows(a.x, a.m, a.xs, (size_t)a.columns * (bf16_out ? 2 : 4));
     } else {
