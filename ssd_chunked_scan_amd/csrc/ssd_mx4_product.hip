@@ -580,12 +580,15 @@ static void mx4_tile_launch(const Mx4ProductArgs &a, hipStream_t stream) {
 // 2560, m = 4096: 60 70 117; 2048: 41 40 74; 1024: 23 24 40; 512: 18 15 23; 256:
 // 17 11 13; 128: 17 10 8; m x 4096 x 512, m = 2048: 11 9 12; 512: 9 6 4.  So 64
 // while two a compute unit hold them all, 256 from 5/8 of the compute units on.
+// fp32 results leave the 256 tiles too few registers, which long rows make up for:
+// 256 / 128 for 16384 x 10576 x 2560 388 349, 8192 x 4096 x 1024 49 37, 16384 x
+// 2560 x 5120 131 138, 16384 x 1024 x 16384 143 157.
 template <typename OUT>
 static void mx4_tile_out(const Mx4ProductArgs &a, hipStream_t stream) {
     const auto tiles = [&](int b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b); };
     if (a.kblocks <= 2 || tiles(64) <= 2 * (int64_t)a.cus)
         hipLaunchKernelGGL((mx4_ring_kernel<OUT>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
-    else if (8 * tiles(256) >= 5 * (int64_t)a.cus)
+    else if (8 * tiles(256) >= 5 * (int64_t)a.cus && (sizeof(OUT) == 2 || a.kblocks > 32))
         mx4_tile_launch<OUT, 256, 256, 128, 64, 1>(a, stream);
     else
         mx4_tile_launch<OUT, 128, 128, 64, 64, 2>(a, stream);
