@@ -540,7 +540,7 @@ typedef struct {
     float *residual_scales;
 } ssd_block_checkpoint_t;
 
-/* x, residual, z, y, residual_out: io dtype; residual_out may be the residual
+/* x, residual, z, y, residual_out: io dtype; residual_out may be a dense residual
  * itself.  checkpoint (nullable): where to write the copies.  No workspace. */
 ssd_status_t ssd_block_norm_fwd(const ssd_block_shape_t *shape, ssd_dtype_t io,
                                 const void *x, const void *residual,
@@ -586,7 +586,8 @@ typedef struct {
     int64_t reserved[4];  /* must be zero                                */
 } ssd_mx4_shape_t;
 
-/* x: io dtype.  rows / 16 * columns / 512, rounded up, is at most 2^24. */
+/* x: io dtype.  rows / 16 times columns / 512, each rounded up, is
+ * less than 2^24. */
 ssd_status_t ssd_mx4_quant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const void *x,
                            void *q, void *scales, void *stream);
 
@@ -598,8 +599,8 @@ ssd_status_t ssd_mx4_dequant(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
 /* y[r][n] = sum_c a[r][c] w[n][c] + bias[n]: a from q and scales [rows], w from
  * wq and wscales [outputs], both of `columns` columns; products of codes exact,
  * sums in fp32, y [rows][outputs] in the io dtype, dense; bias [outputs]
- * fp32, nullable.  rows / 64 * outputs / 64, rounded up, is at most 2^24.
- * No workspace. */
+ * fp32, nullable.  rows / 64 times outputs / 64, each rounded up, is less than
+ * 2^24.  No workspace. */
 ssd_status_t ssd_mx4_matmul(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
                             const void *q, const void *scales,
                             const void *wq, const void *wscales, const float *bias,

@@ -179,6 +179,9 @@ ssd_status_t ssd_block_norm_fwd(const ssd_block_shape_t *shape, ssd_dtype_t io, 
     SSD_TRY(maybe("scale", scale, 4));
     SSD_TRY(need("y", y, e));
     SSD_TRY(need("residual_out", residual_out, e));
+    if (residual_out == residual && shape->rows > 1 && shape->residual_stride > shape->columns)
+        return fail(SSD_ERR_UNSUPPORTED, "residual_out is dense: it cannot be a residual of stride %lld",
+                    (long long)shape->residual_stride);
     if (checkpoint) SSD_TRY(check_checkpoint(checkpoint, z != nullptr));
     ssd::BlockArgs a = block_args(shape, io, x, z, residual, post_weight, pre_weight, scale, (hipStream_t)stream);
     a.y = y;

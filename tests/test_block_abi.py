@@ -135,6 +135,11 @@ def test_block_fwd_pointers(args, status):
     assert call("ssd_block_norm_fwd", block(), *args) == status
 
 
+def test_block_fwd_in_place_is_dense():
+    """Rows of residual_out lie elsewhere than a strided residual's."""
+    assert call("ssd_block_norm_fwd", block(residual_stride=512), *put(FWD, _7=FWD[1])) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("args,ws,status", [
     (put(BWD, _0=None), BIG, NULL), (put(BWD, _1=None), BIG, NULL), (put(BWD, _6=None), BIG, NULL),
     (put(BWD, _9=None), BIG, NULL), (put(BWD, _10=None), BIG, NULL), (put(BWD, _11=None), BIG, NULL),
@@ -176,6 +181,15 @@ def test_mx4_outputs():
     assert call("ssd_mx4_dequant", mx4(outputs=1), *DEQUANT) == UNSUPPORTED
     assert call("ssd_mx4_dequant", mx4(x_stride=256), *DEQUANT) == UNSUPPORTED
     assert call("ssd_mx4_matmul", mx4(outputs=1, x_stride=256), *MATMUL) == UNSUPPORTED
+
+
+def test_mx4_limits():
+    """Fewer than 2^24 workgroups of 16 rows x 512 columns and of 64 x 64 outputs:
+    the size beyond is refused, the last one is not (by its next check)."""
+    for rows, status in ((1 << 28, UNSUPPORTED), ((1 << 28) - 16, NULL)):
+        assert call("ssd_mx4_quant", mx4(rows=rows, columns=512), *put(QUANT, _0=None)) == status
+    for rows, status in ((1 << 16, UNSUPPORTED), ((1 << 16) - 64, NULL)):
+        assert call("ssd_mx4_matmul", mx4(rows=rows, columns=1, outputs=1 << 20), *put(MATMUL, _0=None)) == status
 
 
 @pytest.mark.parametrize("name,args,ws,status", [
