@@ -11,16 +11,26 @@
 
 namespace ssd {
 
+// LDS accesses of any type.
+typedef i32x4 __attribute__((may_alias)) any_i32x4;
+typedef uint32_t __attribute__((may_alias)) any_u32;
+
+// Between a wave's LDS writes and its lanes' reads of one another's: the hardware
+// keeps a wave's LDS accesses in order, the compiler is told to.
+__device__ inline void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 // ------------------------------------------------------------- few tokens
 //
 // Up to 16 MT tokens: bound by the weights, 17/32 byte each.  A workgroup owns
-// 16 NT outputs and its eight waves take the 128-column blocks in turn; the
-// parts are joined through LDS in a fixed order.  16x16x128: lane l brings row l % 16
-// and the 32 columns 32 (l / 16) .. of either operand, 16 bytes and a scale byte;
-// that is also where a lane can quantise 32 activations by itself, without
-// exchanging anything (IN, up to 16 tokens).
-
-constexpr int kFewWaves = 8;
+// 16 NT outputs and its W waves take the 128-column blocks in turn; the parts are
+// joined through LDS in a fixed order.  16x16x128: lane l brings row l % 16 and the
+// 32 columns 32 (l / 16) .. of either operand, 16 bytes and a scale byte.
+// Activations that are not in 4 bits yet (IN, up to 16 tokens) are quantised while
+// the weights come, so they are loaded first (loads complete in order): 16
+// lanes take 128 columns of a row, as ssd_mx4_quant's do, and the wave's codes
+// change lanes through LDS (a lane that quantised the 32 columns it brings
+// would read 64 separate pieces a load: 8 x 2560 x 5120 8.2 us, 16 x 2560 x 8192
+// fp32 20.4).
 
 template <typename OUT>
 __device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, const float (&v)[4], bool wide) {
@@ -37,13 +47,14 @@ __device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, con
     }
 }
 
-template <typename IN, typename OUT, int MT, int NT, bool WIDE>
-__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs a) {
+template <typename IN, typename OUT, int MT, int NT, int W, bool WIDE>
+__global__ __launch_bounds__(64 * W) void mx4_few_kernel(Mx4ProductArgs a) {
     constexpr bool PRE = std::is_same_v<IN, uint8_t>;   // the activations come in 4 bits
     static_assert(PRE || MT == 1, "quantised on the way: up to 16 tokens");
     typedef std::conditional_t<PRE, float, IN> X;
-    __shared__ float red[kFewWaves][NT * MT][64][4];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    __shared__ float red[W][NT * MT][64][4];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[PRE ? 1 : W][1024 + 64];   // 16 rows, then their scale bytes
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int r = lane % 16, g = lane / 16;
     const int n0 = blockIdx.x * 16 * NT;
     const int m = (int)a.m;
@@ -56,63 +67,62 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs 
         wp[j] = a.w + n * a.kblocks * 64 + g * 16;
         wsp[j] = (const uint8_t *)a.ws + n * 4 + g;
     }
-    // two blocks' loads at a time
-    for (int kb0 = wave; kb0 < a.kblocks; kb0 += 2 * kFewWaves) {
-        i32x4 w[2][NT], t[2][MT];
-        int ws[2][NT], ts[2][MT];
-        Pack<X, 8> v[2][PRE ? 1 : 4];
+    for (int kb = wave; kb < a.kblocks; kb += W) {
+        i32x4 w[NT], t[MT];
+        int ws[NT], ts[MT];
+        Pack<X, 8> v[PRE ? 1 : 4];
+        if constexpr (PRE) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int kb = kb0 + u * kFewWaves;
-            if (kb >= a.kblocks) break;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                w[u][j] = *(const i32x4 *)(wp[j] + kb * 64);
-                ws[u][j] = wsp[j][(int64_t)kb * a.n * 4];
+            for (int i = 0; i < MT; ++i) {
+                const int tok = min(i * 16 + r, m - 1);
+                t[i] = *(const i32x4 *)(a.a + ((int64_t)tok * a.kblocks + kb) * 64 + g * 16);
+                ts[i] = ((const uint8_t *)a.as)[((int64_t)kb * m + tok) * 4 + g];
             }
-            if constexpr (PRE) {
+        } else {
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int tok = min(i * 16 + r, m - 1);
-                    t[u][i] = *(const i32x4 *)(a.a + ((int64_t)tok * a.kblocks + kb) * 64 + g * 16);
-                    ts[u][i] = ((const uint8_t *)a.as)[((int64_t)kb * m + tok) * 4 + g];
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < m)
+                    v[i] = mx4_load8<X, WIDE>((const char *)a.x + min(4 * i + g, m - 1) * a.xs, kb * 128 + r * 8, a.columns);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            w[j] = *(const i32x4 *)(wp[j] + kb * 64);
+            ws[j] = wsp[j][(int64_t)kb * a.n * 4];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!PRE) {
+            uint8_t *mine = codes[wave];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < m) {
+                    const uint32_t byte = mx4_scale_byte(quad_max(mx4_most<X>(v[i])));
+                    *(any_u32 *)(mine + (4 * i + g) * 64 + r * 4) = byte == 255u ? 0u : mx4_codes<X>(v[i], mx4_scale(byte));
+                    if (r % 4 == 0) mine[1024 + (4 * i + g) * 4 + r / 4] = (uint8_t)byte;
                 }
-            } else {
-                const char *row = (const char *)a.x + min(r, m - 1) * a.xs;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[u][q] = mx4_load8<X, WIDE>(row, kb * 128 + g * 32 + q * 8, a.columns);
-            }
+            wave_lds_fence();
+            const int tok = min(r, m - 1);
+            t[0] = *(const any_i32x4 *)(mine + tok * 64 + g * 16);
+            ts[0] = mine[1024 + tok * 4 + g];
+            wave_lds_fence();
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (kb0 + u * kFewWaves >= a.kblocks) break;
-            if constexpr (!PRE) {
-                uint32_t most = 0;
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) most = max(most, mx4_most<X>(v[u][q]));
-                const uint32_t byte = mx4_scale_byte(most);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) t[u][0][q] = (int)mx4_codes<X>(v[u][q], mx4_scale(byte));
-                ts[u][0] = (int)byte;
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_operand(w[u][j]), mx4_operand(t[u][i]),
-                                                                                 acc[j][i], 4, 4, 0, ws[u][j], 0, ts[u][i]);
-        }
+            for (int i = 0; i < MT; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_operand(w[j]), mx4_operand(t[i]), acc[j][i], 4,
+                                                                             4, 0, ws[j], 0, ts[i]);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i) *(f32x4 *)red[wave][j * MT + i][lane] = acc[j][i];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * MT * 64; e += 64 * kFewWaves) {
+    for (int e = threadIdx.x; e < NT * MT * 64; e += 64 * W) {
         const int tile = e / 64, l = e % 64;
         f32x4 s = *(const f32x4 *)red[0][tile][l];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) s += *(const f32x4 *)red[w][tile][l];
+        for (int w = 1; w < W; ++w) s += *(const f32x4 *)red[w][tile][l];
         const int t = tile % MT * 16 + l % 16, n = n0 + tile / MT * 16 + l / 16 * 4;
         const float o[4] = {s[0], s[1], s[2], s[3]};
         if (t < m && n < a.n)
@@ -127,9 +137,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4ProductArgs 
 // operands agree.  Operands go through LDS, loaded there directly, in rows of
 // SEG bytes whose 16-byte pieces lie at piece ^ (row / (16 / pieces) % pieces):
 // 16 consecutive rows at one piece meet 16 different bank groups.
-
-// An LDS access of any type.
-typedef i32x4 __attribute__((may_alias)) any_i32x4;
 
 template <typename OUT>
 __device__ inline void put4(uint8_t *to, const float (&f)[4]) {
@@ -288,6 +295,7 @@ __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int til
 #pragma unroll
     for (int part = 0; part < CH::kPerTile; ++part) {
         CH::put(mine, acc, part);
+        wave_lds_fence();
         CH::get(mine, ys, a.n, wm * 32, wn * 32, nleft - wn * 32, part, wide);
     }
 }
@@ -526,6 +534,7 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
                 } else {
                     uint8_t *mine = out + (LW + wave) * kChunk;
                     CH::put(mine, acc[j][i], part);
+                    wave_lds_fence();
                     store(c, mine, wave);
                     lds_sync();
                     store(c, out + ((wave - LW) * 2 + c % 2) * kChunk, wave - LW);
@@ -545,17 +554,22 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
 template <typename IN, typename OUT, int MT, bool WIDE>
 static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
     // Up to four tiles of 16 outputs share a workgroup's activations where that
-    // leaves 5/8 of the compute units one: 1 x 10576 x 2560 7.2 us with four, 7.6
-    // with two, 9.4 with one; 8 x 2560 x 5120 10.9, 8.6 and 7.8.
+    // leaves 5/8 of the compute units one: 16 x 10576 x 2560 6.9 us with four, 7.6
+    // with two, 8.3 with one; 8 x 2560 x 5120 8.5, 5.8 and 5.6.  Fewer outputs than
+    // that are bound by latency, and more waves take their blocks where they also
+    // quantise: 8 x 2560 x 5120 4.7 us with sixteen, 5.6 with eight; quantised
+    // before, 4.5 and 4.3.
     const auto fits = [&](int nt) { return 8 * (int64_t)((a.n + 16 * nt - 1) / (16 * nt)) >= 5 * (int64_t)a.cus; };
-    const auto launch = [&](auto nt) {
-        constexpr int NT = decltype(nt)::value;
-        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, WIDE>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * kFewWaves), 0,
+    const auto launch = [&](auto nt, auto waves) {
+        constexpr int NT = decltype(nt)::value, W = decltype(waves)::value;
+        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, W, WIDE>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), 0,
                            stream, a);
     };
-    if (fits(4)) launch(std::integral_constant<int, 4>{});
-    else if (fits(2)) launch(std::integral_constant<int, 2>{});
-    else launch(std::integral_constant<int, 1>{});
+    const std::integral_constant<int, 8> eight;
+    if (fits(4)) launch(std::integral_constant<int, 4>{}, eight);
+    else if (fits(2)) launch(std::integral_constant<int, 2>{}, eight);
+    else if (!std::is_same_v<IN, uint8_t> && a.kblocks > 8) launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
+    else launch(std::integral_constant<int, 1>{}, eight);
 }
 
 template <typename OUT>
@@ -596,7 +610,7 @@ static void mx4_tile_out(const Mx4ProductArgs &a, hipStream_t stream) {
 
 // Up to 16 tokens are quantised on the way or share the weights' reading with
 // nothing else; up to 32 go the same way where 64 outputs a workgroup would
-// leave half of the compute units idle (32 x 2560 x 5120: 6.7 us, 8.0 in tiles; 32 x
+// leave half of the compute units idle (32 x 2560 x 5120: 6.3 us, 8.0 in tiles; 32 x
 // 10576 x 2560: 7.6 and 5.3).
 static bool mx4_few(const Mx4ProductArgs &a) {
     return a.m <= 16 || (a.m <= 32 && (a.n + 63) / 64 <= a.cus / 2);
