@@ -344,11 +344,12 @@ def layer_bench(wl, inp, args):
     """One JSON line: the operators of a layer around the scan at the
     workload's sizes, each timed per launch with HIP events on its stream.  The
     layer reads a residual stream of half the inner width, norms it, and takes
-    z | x | B | C | dt from one projection's rows (the two projections are the
-    caller's and not timed): convolution of x, B and C out of those rows,
-    ssd_fwd, the gated norm; the gated linear recurrence in the scan's place;
-    their backward passes; and the single-token forms.  GB/s counts each
-    operator's inputs and outputs once."""
+    z | x | B | C | dt from one projection's rows: convolution of x, B and C out
+    of those rows, ssd_fwd, the gated norm; the gated linear recurrence in the
+    scan's place; the two projections in 4 bits; the seam to the next layer as
+    a block norm, with and without 8-bit checkpoints; their backward passes;
+    and the single-token forms.  GB/s counts each operator's inputs and outputs
+    once."""
     import torch
     import ssd_chunked_scan_amd as ssd
     dev = torch.device("cuda:0")
@@ -378,6 +379,11 @@ def layer_bench(wl, inp, args):
     window = torch.zeros(b, W - 1, D, dtype=io, device=dev)
     state = torch.zeros(b, D, device=dev)
     n, m = b * L * D * e, b * L * S * e
+    w_in, w_out = (ssd.ssd_mx4_quant((r(o, i) / i ** 0.5).to(io)) for o, i in ((row, S), (S, D)))
+    w_bytes = [q.numel() + s.numel() for q, s in (w_in, w_out)]
+    gate_s = proj[..., :S]
+    seam = dict(z=gate_s, scale=0.1 * r(S))
+    s_out, kept = ssd.ssd_block_norm_fwd(hidden, stream, sw, sw, checkpoint=True, **seam)[1:]
     runs = {
         "norm_residual": (lambda: ssd.ssd_norm_fwd(hidden, sw, residual=stream), 4 * m),
         "norm_residual_8bit": (lambda: ssd.ssd_norm_quant_fwd(hidden, sw, residual=stream), 3 * m + m // e),
@@ -395,6 +401,19 @@ def layer_bench(wl, inp, args):
         "conv_x_step": (lambda: ssd.ssd_conv_step(tok[:, D:2 * D], wx, window, bias=cb), 8 * b * D * e),
         "glr_step": (lambda: ssd.ssd_glr_step(tok[:, D:2 * D], gate[:, 0], gA, state, bias=gb, z=tok[:, :D]),
                      b * D * (4 * e + 8)),
+        "block_norm": (lambda: ssd.ssd_block_norm_fwd(hidden, stream, sw, sw, **seam), 5 * m),
+        "block_norm_checkpoint": (lambda: ssd.ssd_block_norm_fwd(hidden, stream, sw, sw, checkpoint=kept, **seam),
+                                  5 * m + 3 * m // e),
+        "block_norm_bwd": (lambda: ssd.ssd_block_norm_bwd(hidden, s_out, sw, sw, ds, dresidual_out=stream, **seam), 8 * m),
+        "block_norm_bwd_checkpoint": (lambda: ssd.ssd_block_norm_bwd(None, None, sw, sw, ds, scale=seam["scale"],
+                                                                     dresidual_out=stream, checkpoint=kept),
+                                      5 * m + 3 * m // e),
+        "block_norm_step": (lambda: ssd.ssd_block_norm_fwd(hidden[:, 0], stream[:, 0], sw, sw, z=gate_s[:, 0],
+                                                           scale=seam["scale"]), 5 * b * S * e),
+        "mx4_in": (lambda: ssd.ssd_mx4_linear(hidden, *w_in), m + w_bytes[0] + b * L * row * e),
+        "mx4_out": (lambda: ssd.ssd_mx4_linear(y, *w_out), n + w_bytes[1] + m),
+        "mx4_in_step": (lambda: ssd.ssd_mx4_linear(hidden[:, 0], *w_in), b * S * e + w_bytes[0] + b * row * e),
+        "mx4_out_step": (lambda: ssd.ssd_mx4_linear(y[:, 0], *w_out), b * D * e + w_bytes[1] + b * S * e),
     }
     cuda_stream = torch.cuda.current_stream(dev)
     out = {}

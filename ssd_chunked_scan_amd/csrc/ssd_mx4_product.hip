@@ -317,7 +317,11 @@ __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int til
 //    loads every stage, the other half stores every result, its partner's
 //    chunk by chunk through LDS (293 us before, 262 after).
 //  - `group` rows of tiles column by column, four of them: neighbouring pieces
-//    of y's rows meet in one XCD's L2 (262 us with eight, 218 with four).
+//    of y's rows meet in one XCD's L2 (262 us with eight, 218 with four).  Each such group
+//    begins at another column: y's rows below each other lie a multiple of
+//    large powers of two apart, and side by side the XCDs would write to few of
+//    the memory's channels (new results every time, 259 us before, 247 after;
+//    8192 rows 149 and 131).
 // The stage of an odd last 128 columns is the last 256 once more with the scales
 // of the first half, which has been taken, at 2^-127: a product below 2^-240 in
 // place of each, which fp32 sums round away.
@@ -366,7 +370,8 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
         const int rows = min(group, tiles_m - first), in = id % per;
         Mx4Tile t;
         t.m0 = (int64_t)(first + in % rows) * BM;
-        t.n0 = in / rows * BN;
+        const int col = in / rows + (int)((int64_t)first * tiles_n / tiles_m);
+        t.n0 = (col < tiles_n ? col : col - tiles_n) * BN;
         t.m = (int)min((int64_t)BM, a.m - t.m0);
         t.n = min(BN, a.n - t.n0);
         t.a = a.a + t.m0 * pitch;
