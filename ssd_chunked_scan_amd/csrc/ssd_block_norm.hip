@@ -131,14 +131,33 @@ __device__ inline void kept_values(const Kept<V> &r, float (&f)[V]) {
 }
 
 // The weights of a thread's columns: post * scale and pre, 1 where not given.
-template <int V>
+// With AGAIN they are loaded where they are used and not held for all rows: the
+// compiler is kept from seeing that they are the same every time.
+template <int V, bool AGAIN>
 __device__ inline void block_weights(const BlockArgs &a, int p, float (&w1)[V], float (&w2)[V]) {
+    auto load = [&](const float *from, float (&f)[V]) {
+        const bool given = from != nullptr;
+        const int bytes = given ? a.columns * 4 : 0;
+        if constexpr (AGAIN) asm volatile("" : "+s"(from));
+        const __amdgpu_buffer_rsrc_t rs = row_of(from, 0, 0, bytes);
+        if constexpr (V == 1) {
+            const float t = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, p * 4, 0, 0));
+            f[0] = given ? t : 1.f;
+        } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = min(p * V + v, a.columns - 1);
-        w1[v] = (a.post ? a.post[c] : 1.f) * (a.scale ? a.scale[c] : 1.f);
-        w2[v] = a.pre ? a.pre[c] : 1.f;
-    }
+            for (int v = 0; v < V; v += 4) {
+                const auto t = __builtin_amdgcn_raw_buffer_load_b128(rs, (p * V + v) * 4, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[v + i] = given ? __uint_as_float(t[i]) : 1.f;
+            }
+        }
+    };
+    float scale[V];
+    load(a.post, w1);
+    load(a.scale, scale);
+    load(a.pre, w2);
+#pragma unroll
+    for (int v = 0; v < V; ++v) w1[v] *= scale[v];
 }
 
 template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
@@ -154,7 +173,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
     if (row >= a.rows) return;   // (without WAVE a workgroup has a row)
-    R xr[K], rr[K], zr[K], xn[K], rn[K], zn[K];
+    // Up to 8 columns a thread the weights stay in registers, and so does the
+    // next row on its way; more columns leave room for neither, and the next row
+    // is loaded as soon as this one's registers are free.
+    constexpr bool HOLD = K * V <= 8;
+    R xr[K], rr[K], zr[K], xn[HOLD ? K : 1], rn[HOLD ? K : 1], zn[HOLD ? K : 1];
     auto load = [&](int64_t r, R (&x)[K], R (&s)[K], R (&z)[K]) {
         const __amdgpu_buffer_rsrc_t xb = row_of(a.x, r, a.xs, bytes), sb = row_of(a.residual, r, a.rs, bytes);
         const __amdgpu_buffer_rsrc_t zb = row_of(a.z, r, a.zs, bytes);
@@ -167,14 +190,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
         }
     };
     load(row, xr, rr, zr);
-    constexpr bool HOLD = K * V <= 8;   // the weights stay in registers
     float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V];
     if constexpr (HOLD) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
+        for (int k = 0; k < K; ++k) block_weights<V, false>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
     }
     for (; row < a.rows; row += step) {
-        load(min(row + step, a.rows - 1), xn, rn, zn);
+        if constexpr (HOLD) load(min(row + step, a.rows - 1), xn, rn, zn);
         float val[K][V], sum[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -202,7 +224,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
+            if constexpr (!HOLD) block_weights<V, true>(a, p, w1[0], w2[0]);
             float st[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -222,30 +244,80 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
         if constexpr (CKPT)
             store_checkpoint<V, K>(row_of(a.sq, row, a.columns, a.columns), row_of(a.ssc, row, nscale * 4, nscale * 4), val, tid,
                                    nthr);
+        if constexpr (!HOLD) load(min(row + step, a.rows - 1), xr, rr, zr);
         row_sums<WAVE, 1>(sum, lds[1]);
         const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
         const __amdgpu_buffer_rsrc_t yb = row_of(a.y, row, dense, bytes);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
+            if constexpr (!HOLD) block_weights<V, true>(a, p, w1[0], w2[0]);
 #pragma unroll
             for (int v = 0; v < V; ++v) val[k][v] = val[k][v] * rstd2 * w2[HOLD ? k : 0][v];
             buffer_store<IO, V>(yb, (uint32_t)(p * (V * E)), 0, val[k]);
         }
+        if constexpr (HOLD) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            xr[k] = xn[k];
-            rr[k] = rn[k];
-            zr[k] = zn[k];
+            for (int k = 0; k < K; ++k) {
+                xr[k] = xn[k];
+                rr[k] = rn[k];
+                zr[k] = zn[k];
+            }
         }
     }
 }
 
+// A thread's column sums: in registers for few columns, else in LDS, each
+// thread's own places, 16 bytes side by side.
+template <int V, int K, bool REGISTERS>
+struct ColumnSums {
+    float r[REGISTERS ? K : 1][V];
+    float *lds;
+    static constexpr int kFloats = REGISTERS ? 1 : 1024 * K * V;
+
+    __device__ inline void clear() {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float zero[V] = {};
+            put(k, zero);
+        }
+    }
+    __device__ inline void get(int k, float (&f)[V]) const {
+        if constexpr (REGISTERS) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = r[k][v];
+        } else if constexpr (V == 1) {
+            f[0] = lds[k * 1024 + threadIdx.x];
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const f32x4 t = *(const f32x4 *)(lds + ((k * V + v) / 4 * 1024 + threadIdx.x) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[v + i] = t[i];
+            }
+        }
+    }
+    __device__ inline void put(int k, const float (&f)[V]) {
+        if constexpr (REGISTERS) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[k][v] = f[v];
+        } else if constexpr (V == 1) {
+            lds[k * 1024 + threadIdx.x] = f[0];
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v += 4)
+                *(f32x4 *)(lds + ((k * V + v) / 4 * 1024 + threadIdx.x) * 4) = f32x4{f[v], f[v + 1], f[v + 2], f[v + 3]};
+        }
+    }
+};
+
+// Single columns take more registers, for their addresses.
+constexpr bool block_bwd_holds(int K, int V) { return K * V <= (V == 1 ? 4 : 8); }
+
 // Backward: a.parts workgroups take the rows in turn and keep their columns'
-// two sums in registers; each leaves a row of parts [2][columns]: m, dpre.
+// two sums; each leaves a row of parts [2][columns]: m, dpre.
 template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
-__global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_bwd_kernel(BlockArgs a) {
+__global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) void block_bwd_kernel(BlockArgs a) {
     typedef Raw<IO, V> RW;
     typedef typename RW::type R;
     constexpr int RPB = WAVE ? 4 : 1;
@@ -256,13 +328,18 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int nscale = (a.columns + 127) / 128, bytes = a.columns * E, dense = bytes;
     const float inv_n = 1.f / (float)a.columns;
-    constexpr bool HOLD = K * V <= 8;
-    float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V], dm[K][V], dp[K][V];
+    constexpr bool HOLD = block_bwd_holds(K, V);   // weights and sums in registers
+    float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V];
+    typedef ColumnSums<V, K, HOLD> CS;
+    __shared__ __attribute__((aligned(16))) float column_sums[2][CS::kFloats];
+    CS dm, dp;
+    dm.lds = column_sums[0];
+    dp.lds = column_sums[1];
+    dm.clear();
+    dp.clear();
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        if constexpr (HOLD) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) dm[k][v] = dp[k][v] = 0.f;
+        for (int k = 0; k < K; ++k) block_weights<V, false>(a, pack_at<V>(k, tid, nthr), w1[k], w2[k]);
     }
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? wave : 0);
@@ -313,7 +390,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
         float n1[K][V], h[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if constexpr (!HOLD) block_weights<V>(a, pack_at<V>(k, tid, nthr), w1[0], w2[0]);
+            if constexpr (!HOLD) block_weights<V, true>(a, pack_at<V>(k, tid, nthr), w1[0], w2[0]);
             float s[V];
             value(xr, xk, k, n1[k]);
             value(sr, sk, k, s);
@@ -333,15 +410,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
-            if constexpr (!HOLD) block_weights<V>(a, p, w1[0], w2[0]);
-            float s[V], z[V], dr[V], dz[V];
+            if constexpr (!HOLD) block_weights<V, true>(a, p, w1[0], w2[0]);
+            float s[V], z[V], dr[V], dz[V], m[V], q[V];
+            dm.get(k, m);
+            dp.get(k, q);
             value(sr, sk, k, s);
             if (GATE) value(zr, zk, k, z);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float c = w1[HOLD ? k : 0][v], w = w2[HOLD ? k : 0][v];
                 const float dy = RW::at(yr[k], v), n2 = s[v] * rstd2;
-                dp[k][v] = fmaf(dy, n2, dp[k][v]);
+                q[v] = fmaf(dy, n2, q[v]);
                 const float ds = fmaf(rstd2, fmaf(-n2, mean2, w * dy), RW::at(gr[k], v));
                 dr[v] = a.alpha * ds;
                 n1[k][v] *= rstd1;
@@ -351,10 +430,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
                     dz[v] = ds * c * n1[k][v] * (sig * fmaf(z[v], 1.f - sig, 1.f));
                     t = ds * (z[v] * sig);
                 }
-                dm[k][v] = fmaf(t, n1[k][v], dm[k][v]);
+                m[v] = fmaf(t, n1[k][v], m[v]);
                 h[k][v] = t * c;
                 sum[0] = fmaf(h[k][v], n1[k][v], sum[0]);
             }
+            dm.put(k, m);
+            dp.put(k, q);
             buffer_store<IO, V>(rb, (uint32_t)(p * (V * E)), 0, dr);
             if (GATE) buffer_store<IO, V>(zb, (uint32_t)(p * (V * E)), 0, dz);
         }
@@ -383,17 +464,20 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, K * V <= 8 ? 4 : 1) void block_b
                 to[c] = ((red[0][c] + red[1][c]) + red[2][c]) + red[3][c];
             __syncthreads();
         };
-        join(dm, out);
-        join(dp, out + a.columns);
+        join(dm.r, out);
+        join(dp.r, out + a.columns);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int p = pack_at<V>(k, tid, nthr);
+            float m[V], q[V];
+            dm.get(k, m);
+            dp.get(k, q);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (p * V < a.columns) {
-                    out[p * V + v] = dm[k][v];
-                    out[a.columns + p * V + v] = dp[k][v];
+                    out[p * V + v] = m[v];
+                    out[a.columns + p * V + v] = q[v];
                 }
         }
     }
@@ -456,35 +540,38 @@ static void block_bwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
 #undef SSD_BLOCK_BWD
 }
 
-// As the norm's kernels: a wave per row where it can hold KW packs a lane, a
-// workgroup of KB packs a thread while 1024 threads can hold the row, else of KX.
+// As the norm's kernels: a wave per row where it can hold KW packs a lane, else a
+// workgroup of KB, KM or KX packs a thread, the first with which 1024 threads can
+// hold the row.
 #define SSD_BLOCK_SHAPE(launch)                                        \
     const int npack = a.columns / V;                                   \
     if (npack <= 64 * KW)                                              \
         launch<IO, V, true, KW>(a, stream, 256);                       \
     else if (npack <= 1024 * KB)                                       \
         launch<IO, V, false, KB>(a, stream, norm_threads(npack, KB));  \
+    else if (npack <= 1024 * KM)                                       \
+        launch<IO, V, false, KM>(a, stream, norm_threads(npack, KM));  \
     else                                                               \
         launch<IO, V, false, KX>(a, stream, norm_threads(npack, KX));
 
-template <typename IO, int V, int KW, int KB, int KX>
+template <typename IO, int V, int KW, int KB, int KM, int KX>
 static void block_fwd_shape(const BlockArgs &a, hipStream_t stream) { SSD_BLOCK_SHAPE(block_fwd_launch) }
 
-template <typename IO, int V, int KW, int KB, int KX>
+template <typename IO, int V, int KW, int KB, int KM, int KX>
 static void block_bwd_shape(const BlockArgs &a, hipStream_t stream) { SSD_BLOCK_SHAPE(block_bwd_launch) }
 
 void launch_block_fwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {
     if (bf16_io)
-        wide ? block_fwd_shape<bf16, 8, 1, 1, 2>(a, stream) : block_fwd_shape<bf16, 1, 8, 8, 16>(a, stream);
+        wide ? block_fwd_shape<bf16, 8, 1, 1, 1, 2>(a, stream) : block_fwd_shape<bf16, 1, 8, 8, 8, 16>(a, stream);
     else
-        wide ? block_fwd_shape<float, 4, 2, 2, 4>(a, stream) : block_fwd_shape<float, 1, 8, 8, 16>(a, stream);
+        wide ? block_fwd_shape<float, 4, 2, 2, 2, 4>(a, stream) : block_fwd_shape<float, 1, 8, 8, 8, 16>(a, stream);
 }
 
 void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {
     if (bf16_io)
-        wide ? block_bwd_shape<bf16, 8, 1, 1, 2>(a, stream) : block_bwd_shape<bf16, 1, 4, 4, 16>(a, stream);
+        wide ? block_bwd_shape<bf16, 8, 1, 1, 1, 2>(a, stream) : block_bwd_shape<bf16, 1, 4, 4, 8, 16>(a, stream);
     else
-        wide ? block_bwd_shape<float, 4, 2, 2, 4>(a, stream) : block_bwd_shape<float, 1, 4, 4, 16>(a, stream);
+        wide ? block_bwd_shape<float, 4, 2, 2, 2, 4>(a, stream) : block_bwd_shape<float, 1, 4, 4, 8, 16>(a, stream);
     if (a.part) hipLaunchKernelGGL(block_finish_kernel, dim3((a.columns + kFinish - 1) / kFinish * 2), dim3(1024), 0, stream, a);
 }
 
