@@ -8,9 +8,9 @@
 namespace ssd {
 void launch_block_fwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream);
 void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream);
-void launch_mx4_quant(bool bf16_io, bool wide, const Mx4QuantArgs &a, hipStream_t stream);
-void launch_mx4_dequant(bool bf16_io, bool wide, const Mx4QuantArgs &a, hipStream_t stream);
-void launch_mx4_product(bool bf16_out, bool wide, const Mx4ProductArgs &a, hipStream_t stream);
+void launch_mx4_quant(bool bf16_io, const Mx4QuantArgs &a, hipStream_t stream);
+void launch_mx4_dequant(bool bf16_io, const Mx4QuantArgs &a, hipStream_t stream);
+void launch_mx4_product(bool bf16_out, const Mx4ProductArgs &a, hipStream_t stream);
 }  // namespace ssd
 
 namespace {
@@ -139,8 +139,6 @@ ssd::Mx4QuantArgs quant_args(const ssd_mx4_shape_t *s, ssd_dtype_t io) {
     return a;
 }
 
-bool quant_wide(const ssd::Mx4QuantArgs &a) { return aligned(a.x, 16) && a.xs % 16 == 0; }
-
 ssd::Mx4ProductArgs product_args(const ssd_mx4_shape_t *s, const void *wq, const void *wscales, const float *bias,
                                  void *y, hipStream_t stream) {
     ssd::Mx4ProductArgs a = {};
@@ -265,7 +263,7 @@ ssd_status_t ssd_mx4_quant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const v
     a.q = (uint8_t *)q;
     a.scales = (uint32_t *)scales;
     (void)hipGetLastError();   // not an earlier call's
-    ssd::launch_mx4_quant(io == SSD_BF16, quant_wide(a), a, (hipStream_t)stream);
+    ssd::launch_mx4_quant(io == SSD_BF16, a, (hipStream_t)stream);
     return launched("ssd_mx4_quant");
 }
 
@@ -279,9 +277,8 @@ ssd_status_t ssd_mx4_dequant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const
     a.q = (uint8_t *)q;
     a.scales = (uint32_t *)scales;
     a.y = y;
-    const bool wide = aligned(y, 16) && shape->columns * io_size(io) % 16 == 0;
     (void)hipGetLastError();   // not an earlier call's
-    ssd::launch_mx4_dequant(io == SSD_BF16, wide, a, (hipStream_t)stream);
+    ssd::launch_mx4_dequant(io == SSD_BF16, a, (hipStream_t)stream);
     return launched("ssd_mx4_dequant");
 }
 
@@ -297,7 +294,7 @@ ssd_status_t ssd_mx4_matmul(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const 
     a.a = (const uint8_t *)q;
     a.as = (const uint32_t *)scales;
     (void)hipGetLastError();   // not an earlier call's
-    ssd::launch_mx4_product(io == SSD_BF16, true, a, (hipStream_t)stream);
+    ssd::launch_mx4_product(io == SSD_BF16, a, (hipStream_t)stream);
     return launched("ssd_mx4_matmul");
 }
 
@@ -322,14 +319,14 @@ ssd_status_t ssd_mx4_linear(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const 
     if (bytes == 0) {
         a.x = x;
         a.xs = qa.xs;
-        ssd::launch_mx4_product(io == SSD_BF16, quant_wide(qa), a, (hipStream_t)stream);
+        ssd::launch_mx4_product(io == SSD_BF16, a, (hipStream_t)stream);
     } else {
         qa.q = (uint8_t *)workspace;
         qa.scales = (uint32_t *)((char *)workspace + linear_codes(shape));
-        ssd::launch_mx4_quant(io == SSD_BF16, quant_wide(qa), qa, (hipStream_t)stream);
+        ssd::launch_mx4_quant(io == SSD_BF16, qa, (hipStream_t)stream);
         a.a = qa.q;
         a.as = qa.scales;
-        ssd::launch_mx4_product(io == SSD_BF16, true, a, (hipStream_t)stream);
+        ssd::launch_mx4_product(io == SSD_BF16, a, (hipStream_t)stream);
     }
     return launched("ssd_mx4_linear");
 }

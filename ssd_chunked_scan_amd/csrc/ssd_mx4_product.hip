@@ -33,21 +33,22 @@ __device__ inline void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_RE
 // fp32 20.4).
 
 template <typename OUT>
-__device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, const float (&v)[4], bool wide) {
+__device__ inline void mx4_store4(const Mx4ProductArgs &a, int64_t t, int n, const float (&v)[4]) {
     OUT *y = (OUT *)a.y + t * a.n + n;
-    float o[4];
+    Pack<OUT, 4> o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = v[i] + (a.bias && n + i < a.n ? a.bias[n + i] : 0.f);
-    if (wide) {
-        store_pack<OUT, 4>(y, o);
+    for (int i = 0; i < 4; ++i) o.v[i] = (OUT)(v[i] + (a.bias && n + i < a.n ? a.bias[n + i] : 0.f));
+    if (n + 4 <= a.n) {
+        typedef uint32_t __attribute__((ext_vector_type(sizeof(OUT)), aligned(sizeof(OUT)), may_alias)) four;
+        *(four *)y = __builtin_bit_cast(four, o);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n + i < a.n) y[i] = (OUT)o[i];
+            if (n + i < a.n) y[i] = o.v[i];
     }
 }
 
-template <typename IN, typename OUT, int MT, int NT, int W, bool WIDE>
+template <typename IN, typename OUT, int MT, int NT, int W>
 __global__ __launch_bounds__(64 * W) void mx4_few_kernel(Mx4ProductArgs a) {
     constexpr bool PRE = std::is_same_v<IN, uint8_t>;   // the activations come in 4 bits
     static_assert(PRE || MT == 1, "quantised on the way: up to 16 tokens");
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(64 * W) void mx4_few_kernel(Mx4ProductArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (4 * i < m)
-                    v[i] = mx4_load8<X, WIDE>((const char *)a.x + min(4 * i + g, m - 1) * a.xs, kb * 128 + r * 8, a.columns);
+                    v[i] = mx4_load8<X>((const char *)a.x + min(4 * i + g, m - 1) * a.xs, kb * 128 + r * 8, a.columns);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -125,8 +126,7 @@ __global__ __launch_bounds__(64 * W) void mx4_few_kernel(Mx4ProductArgs a) {
         for (int w = 1; w < W; ++w) s += *(const f32x4 *)red[w][tile][l];
         const int t = tile % MT * 16 + l % 16, n = n0 + tile / MT * 16 + l / 16 * 4;
         const float o[4] = {s[0], s[1], s[2], s[3]};
-        if (t < m && n < a.n)
-            mx4_store4<OUT>(a, t, n, o, a.n % 4 == 0 && (uintptr_t)a.y % (4 * sizeof(OUT)) == 0);
+        if (t < m && n < a.n) mx4_store4<OUT>(a, t, n, o);
     }
 }
 
@@ -149,19 +149,36 @@ __device__ inline void put4(uint8_t *to, const float (&f)[4]) {
     }
 }
 
-// A 16-byte piece of a row of y, `left` outputs before the row's end; a lane
-// past the last row or output stores nothing (its offset is outside ys).
-template <typename OUT>
-__device__ inline void store_piece(__amdgpu_buffer_rsrc_t ys, uint32_t at, int left, i32x4 v, bool wide) {
+// Rows of y from an output on.
+struct Mx4Rows {
+    __amdgpu_buffer_rsrc_t rs;   // ends with the last row
+    uint8_t *base;
+    int rows;
+};
+
+// A 16-byte piece `at` bytes on in a row of y, `left` outputs before the row's end;
+// a lane past the last row or output stores nothing (its offset is outside the
+// descriptor).  Pieces of fp32 are aligned to 4 bytes at least, which is all that
+// a buffer's store asks for; those of bf16 that are not (WIDE) go by the address,
+// which may be any (4096 x 2561 x 2560 bf16: 28 us, output by output 47.5).
+template <typename OUT, bool WIDE>
+__device__ inline void store_piece(const Mx4Rows &y, int row, uint32_t at, int left, i32x4 v) {
     constexpr int V = 16 / (int)sizeof(OUT);
-    if (wide) {
-        __builtin_amdgcn_raw_buffer_store_b128(v, ys, left > 0 ? at : 0xffffffffu, 0, 0);
-    } else {
+    if constexpr (WIDE) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, y.rs, left > 0 ? at : 0xffffffffu, 0, 0);
+        return;
+    }
+    if constexpr (sizeof(OUT) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, y.rs, left >= V ? at : 0xffffffffu, 0, 0);
+    } else if (left >= V && row < y.rows) {
+        *(mx4_piece<OUT> *)(y.base + at) = __builtin_bit_cast(mx4_piece<OUT>, v);
+    }
+    if (left > 0 && left < V) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const uint32_t ok = left > e ? at + e * (uint32_t)sizeof(OUT) : 0xffffffffu;
-            if constexpr (sizeof(OUT) == 4) __builtin_amdgcn_raw_buffer_store_b32(v[e], ys, ok, 0, 0);
-            else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2))), ys, ok, 0, 0);
+            if constexpr (sizeof(OUT) == 4) __builtin_amdgcn_raw_buffer_store_b32(v[e], y.rs, ok, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2))), y.rs, ok, 0, 0);
         }
     }
 }
@@ -177,7 +194,7 @@ __device__ inline __amdgpu_buffer_rsrc_t bounded(const void *base, uint32_t byte
 // pieces at piece ^ (token / 4 % 4), and read back in whole rows.
 constexpr int kChunk = 2048;
 
-template <typename OUT>
+template <typename OUT, bool WIDE>
 struct Mx4Chunk {
     static constexpr int kGroups = sizeof(OUT) == 2 ? 4 : 2;   // of 8 outputs
     static constexpr int kPerTile = 4 / kGroups;
@@ -194,30 +211,25 @@ struct Mx4Chunk {
 
     // To y's rows from ys on; `row` the chunk's first one, n0 its tile's first
     // output and `left` what is left of the row from there.
-    static __device__ inline void get(const uint8_t *from, __amdgpu_buffer_rsrc_t ys, int pitch, int row, int n0, int left,
-                                      int part, bool wide) {
+    static __device__ inline void get(const uint8_t *from, const Mx4Rows &y, int pitch, int row, int n0, int left,
+                                      int part) {
         const int lane = threadIdx.x % 64;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int t = p * 16 + lane / 4, n = part * kGroups * 8 + lane % 4 * V;
             const i32x4 v = *(const any_i32x4 *)(from + t * 64 + ((lane % 4) ^ (t / 4 % 4)) * 16);
             const uint32_t at = ((uint32_t)(row + t) * (uint32_t)pitch + (uint32_t)(n0 + n)) * (uint32_t)sizeof(OUT);
-            store_piece<OUT>(ys, at, left - n, v, wide);
+            store_piece<OUT, WIDE>(y, row + t, at, left - n, v);
         }
     }
 };
 
-// Whether 16-byte stores are aligned in y.
-template <typename OUT>
-__device__ inline bool stores_wide(const Mx4ProductArgs &a) {
-    return a.n % (16 / (int)sizeof(OUT)) == 0 && (uintptr_t)a.y % 16 == 0;
-}
-
 // y's rows from t0 on, `rows` of them (none if negative), from output n0 on.
 template <typename OUT>
-__device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const Mx4ProductArgs &a, int64_t t0, int rows, int n0) {
-    return bounded((OUT *)a.y + t0 * a.n + n0,
-                   rows > 0 ? ((uint32_t)rows * (uint32_t)a.n - (uint32_t)n0) * (uint32_t)sizeof(OUT) : 0u);
+__device__ inline Mx4Rows rows_of_y(const Mx4ProductArgs &a, int64_t t0, int rows, int n0) {
+    OUT *base = (OUT *)a.y + t0 * a.n + n0;
+    return {bounded(base, rows > 0 ? ((uint32_t)rows * (uint32_t)a.n - (uint32_t)n0) * (uint32_t)sizeof(OUT) : 0u),
+            (uint8_t *)base, rows};
 }
 
 // Problems of few tiles, whose time is the latency of their loads: a workgroup of
@@ -226,7 +238,7 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const Mx4ProductArgs &a, int6
 // one on its way; 128 x 2560 x 5120: 8.0 and 10.4).  An empty kernel takes 1.6.
 constexpr int kRing = 4;
 
-template <typename OUT>
+template <typename OUT, bool WIDE>
 __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int tiles_n) {
     constexpr int ROWS = 128, CODES = ROWS * 128, STAGE = CODES + ROWS * 8, LOADS = 5;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * STAGE];
@@ -288,15 +300,14 @@ __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int til
         buf = buf == kRing - 1 ? 0 : buf + 1;
     }
     vmem_lds_sync();
-    typedef Mx4Chunk<OUT> CH;
+    typedef Mx4Chunk<OUT, WIDE> CH;
     uint8_t *mine = lds + wave * kChunk;
-    const __amdgpu_buffer_rsrc_t ys = rows_of_y<OUT>(a, m0, mleft, n0);
-    const bool wide = stores_wide<OUT>(a);
+    const Mx4Rows ys = rows_of_y<OUT>(a, m0, mleft, n0);
 #pragma unroll
     for (int part = 0; part < CH::kPerTile; ++part) {
         CH::put(mine, acc, part);
         wave_lds_fence();
-        CH::get(mine, ys, a.n, wm * 32, wn * 32, nleft - wn * 32, part, wide);
+        CH::get(mine, ys, a.n, wm * 32, wn * 32, nleft - wn * 32, part);
     }
 }
 
@@ -340,11 +351,11 @@ struct Mx4Tile {
     int n0;
 };
 
-template <typename OUT, int BM, int BN, int WM, int WN, int PERCU>
+template <typename OUT, int BM, int BN, int WM, int WN, int PERCU, bool WIDE>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), PERCU * (BM / WM) * (BN / WN) / 4)
 void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
     typedef Mx4Stage<BM, BN> ST;
-    typedef Mx4Chunk<OUT> CH;
+    typedef Mx4Chunk<OUT, WIDE> CH;
     constexpr int W = (BM / WM) * (BN / WN), LW = W / 2;   // waves, and those of them that load
     constexpr int TM = WM / 32, TN = WN / 32, N = TN * TM, READS = TN + TM;
     constexpr int LA = BM / 8 / LW, LB = BN / 8 / LW, PARTS = ST::kRows / 64, LS = 2 * PARTS / LW, LOADS = LA + LB + LS;
@@ -444,7 +455,6 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
             __builtin_amdgcn_sched_barrier(0x6);   // only arithmetic moves across
         }
     };
-    const bool wide = stores_wide<OUT>(a);
     auto walk = [&](auto role) {
         constexpr bool LOADER = decltype(role)::value;
         Mx4Tile cur = place(begin);
@@ -528,7 +538,7 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
                 const int i = c / CH::kPerTile / TN, j = c / CH::kPerTile % TN;
                 const int om = of % (BM / WM) * WM, on = of / (BM / WM) * WN + 32 * j;
                 CH::get(from, rows_of_y<OUT>(a, cur.m0 + om, min(WM, cur.m - om), cur.n0), a.n, 32 * i, on, cur.n - on,
-                        c % CH::kPerTile, wide);
+                        c % CH::kPerTile);
             };
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -556,7 +566,7 @@ void mx4_tile_kernel(Mx4ProductArgs a, int tiles_m, int tiles_n, int group) {
 
 // ---------------------------------------------------------------- launches
 
-template <typename IN, typename OUT, int MT, bool WIDE>
+template <typename IN, typename OUT, int MT>
 static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
     // Up to four tiles of 16 outputs share a workgroup's activations where that
     // leaves 5/8 of the compute units one: 16 x 10576 x 2560 6.9 us with four, 7.6
@@ -567,7 +577,7 @@ static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
     const auto fits = [&](int nt) { return 8 * (int64_t)((a.n + 16 * nt - 1) / (16 * nt)) >= 5 * (int64_t)a.cus; };
     const auto launch = [&](auto nt, auto waves) {
         constexpr int NT = decltype(nt)::value, W = decltype(waves)::value;
-        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, W, WIDE>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), 0,
+        hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, W>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), 0,
                            stream, a);
     };
     const std::integral_constant<int, 8> eight;
@@ -578,19 +588,19 @@ static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
 }
 
 template <typename OUT>
-static void mx4_few_out(bool wide, const Mx4ProductArgs &a, hipStream_t stream) {
+static void mx4_few_out(const Mx4ProductArgs &a, hipStream_t stream) {
     if (a.x) {
-        wide ? mx4_few_launch<OUT, OUT, 1, true>(a, stream) : mx4_few_launch<OUT, OUT, 1, false>(a, stream);
+        mx4_few_launch<OUT, OUT, 1>(a, stream);
     } else {
-        a.m <= 16 ? mx4_few_launch<uint8_t, OUT, 1, true>(a, stream) : mx4_few_launch<uint8_t, OUT, 2, true>(a, stream);
+        a.m <= 16 ? mx4_few_launch<uint8_t, OUT, 1>(a, stream) : mx4_few_launch<uint8_t, OUT, 2>(a, stream);
     }
 }
 
-template <typename OUT, int BM, int BN, int WM, int WN, int PERCU>
+template <typename OUT, int BM, int BN, int WM, int WN, int PERCU, bool WIDE>
 static void mx4_tile_launch(const Mx4ProductArgs &a, hipStream_t stream) {
     const int tm = (int)((a.m + BM - 1) / BM), tn = (a.n + BN - 1) / BN;
     const int64_t grid = std::min((int64_t)tm * tn, (int64_t)PERCU * a.cus);
-    hipLaunchKernelGGL((mx4_tile_kernel<OUT, BM, BN, WM, WN, PERCU>), dim3((unsigned)grid), dim3(64 * (BM / WM) * (BN / WN)), 0,
+    hipLaunchKernelGGL((mx4_tile_kernel<OUT, BM, BN, WM, WN, PERCU, WIDE>), dim3((unsigned)grid), dim3(64 * (BM / WM) * (BN / WN)), 0,
                        stream, a, tm, tn, 4);
 }
 
@@ -599,18 +609,20 @@ static void mx4_tile_launch(const Mx4ProductArgs &a, hipStream_t stream) {
 // 2560, m = 4096: 60 70 117; 2048: 41 40 74; 1024: 23 24 40; 512: 18 15 23; 256:
 // 17 11 13; 128: 17 10 8; m x 4096 x 512, m = 2048: 11 9 12; 512: 9 6 4.  So 64
 // while two a compute unit hold them all, 256 from 5/8 of the compute units on.
-// fp32 results leave the 256 tiles too few registers, which long rows make up for:
-// 256 / 128 for 16384 x 10576 x 2560 388 349, 8192 x 4096 x 1024 49 37, 16384 x
-// 2560 x 5120 131 138, 16384 x 1024 x 16384 143 157.
-template <typename OUT>
+// fp32 results, and bf16 ones in pieces that are not aligned, leave the 256 tiles
+// too few registers on their way out, which long rows make up for: 256 / 128 for
+// fp32 16384 x 10576 x 2560 344 340, 8192 x 4096 x 1024 53 44, 16384 x 2560 x
+// 5120 141 164, 8192 x 8192 x 8192 278 335; bf16 8192 x 4097 x 1024 46 34, 4096 x
+// 2561 x 2560 28 26, 16384 x 10577 x 2560 287 307, 16384 x 2561 x 5120 142 157.
+template <typename OUT, bool WIDE>
 static void mx4_tile_out(const Mx4ProductArgs &a, hipStream_t stream) {
     const auto tiles = [&](int b) { return ((a.m + b - 1) / b) * ((a.n + b - 1) / b); };
     if (a.kblocks <= 2 || tiles(64) <= 2 * (int64_t)a.cus)
-        hipLaunchKernelGGL((mx4_ring_kernel<OUT>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
-    else if (8 * tiles(256) >= 5 * (int64_t)a.cus && (sizeof(OUT) == 2 || a.kblocks > 32))
-        mx4_tile_launch<OUT, 256, 256, 128, 64, 1>(a, stream);
+        hipLaunchKernelGGL((mx4_ring_kernel<OUT, WIDE>), dim3((unsigned)tiles(64)), dim3(256), 0, stream, a, (a.n + 63) / 64);
+    else if (8 * tiles(256) >= 5 * (int64_t)a.cus && a.kblocks > (sizeof(OUT) == 4 ? 32 : WIDE ? 0 : 16))
+        mx4_tile_launch<OUT, 256, 256, 128, 64, 1, WIDE>(a, stream);
     else
-        mx4_tile_launch<OUT, 128, 128, 64, 64, 2>(a, stream);
+        mx4_tile_launch<OUT, 128, 128, 64, 64, 2, WIDE>(a, stream);
 }
 
 // Up to 16 tokens are quantised on the way or share the weights' reading with
@@ -621,11 +633,15 @@ static bool mx4_few(const Mx4ProductArgs &a) {
     return a.m <= 16 || (a.m <= 32 && (a.n + 63) / 64 <= a.cus / 2);
 }
 
-void launch_mx4_product(bool bf16_out, bool wide, const Mx4ProductArgs &a, hipStream_t stream) {
+void launch_mx4_product(bool bf16_out, const Mx4ProductArgs &a, hipStream_t stream) {
+    const int size = bf16_out ? 2 : 4;
+    const bool wide = (uintptr_t)a.y % 16 == 0 && (int64_t)a.n * size % 16 == 0;   // every 16-byte piece of y aligned
     if (mx4_few(a))
-        bf16_out ? mx4_few_out<bf16>(wide, a, stream) : mx4_few_out<float>(wide, a, stream);
+        bf16_out ? mx4_few_out<bf16>(a, stream) : mx4_few_out<float>(a, stream);
+    else if (wide)
+        bf16_out ? mx4_tile_out<bf16, true>(a, stream) : mx4_tile_out<float, true>(a, stream);
     else
-        bf16_out ? mx4_tile_out<bf16>(a, stream) : mx4_tile_out<float>(a, stream);
+        bf16_out ? mx4_tile_out<bf16, false>(a, stream) : mx4_tile_out<float, false>(a, stream);
 }
 
 }  // namespace ssd

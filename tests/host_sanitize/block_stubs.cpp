@@ -90,21 +90,21 @@ void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t) 
     wr(a.dscale, 4 * D);
 }
 
-void launch_mx4_quant(bool bf16_io, bool, const Mx4QuantArgs &a, hipStream_t) {
+void launch_mx4_quant(bool bf16_io, const Mx4QuantArgs &a, hipStream_t) {
     ++g_block_launches;
     rd_rows(a.x, a.rows, a.xs, (size_t)a.columns * (bf16_io ? 2 : 4));
     wr(a.q, (size_t)a.rows * a.kblocks * 64);
     wr(a.scales, (size_t)a.rows * a.kblocks * 4);
 }
 
-void launch_mx4_dequant(bool bf16_io, bool, const Mx4QuantArgs &a, hipStream_t) {
+void launch_mx4_dequant(bool bf16_io, const Mx4QuantArgs &a, hipStream_t) {
     ++g_block_launches;
     rd(a.q, (size_t)a.rows * a.kblocks * 64);
     rd(a.scales, (size_t)a.rows * a.kblocks * 4);
     wr(a.y, (size_t)a.rows * a.columns * (bf16_io ? 2 : 4));
 }
 
-void launch_mx4_product(bool bf16_out, bool, const Mx4ProductArgs &a, hipStream_t) {
+void launch_mx4_product(bool bf16_out, const Mx4ProductArgs &a, hipStream_t) {
     ++g_block_launches;
     if (a.cus <= 0 || !a.x == !a.a || (a.x && a.m > 16)) __builtin_trap();
     if (a.x) {
