@@ -238,6 +238,20 @@ __device__ inline Mx4Rows rows_of_y(const Mx4ProductArgs &a, int64_t t0, int row
 // one on its way; 128 x 2560 x 5120: 8.0 and 10.4).  An empty kernel takes 1.6.
 constexpr int kRing = 4;
 
+// vmem_lds_sync_lookahead in a loop around a ring of tiles: the KEEP newest
+// operations are the direct-to-LDS loads of several later tiles, issued in earlier
+// rounds of the loop or before it.  The build check follows every path back
+// from the wait.
+template <int KEEP>
+__device__ inline void vmem_lds_sync_ring() {
+    static_assert(KEEP > 0 && KEEP < 64, "vmcnt range");
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    asm volatile("; ssd ring wait" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(KEEP));
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 template <typename OUT, bool WIDE>
 __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int tiles_n) {
     constexpr int ROWS = 128, CODES = ROWS * 128, STAGE = CODES + ROWS * 8, LOADS = 5;

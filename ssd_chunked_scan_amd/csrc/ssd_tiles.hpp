@@ -99,19 +99,6 @@ __device__ inline void vmem_lds_sync_lookahead() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// The same in a loop around a ring of tiles: the KEEP newest operations are the
-// direct-to-LDS loads of several later tiles, issued in earlier rounds of the loop
-// or before it.  The build check follows every path back from the wait.
-template <int KEEP>
-__device__ inline void vmem_lds_sync_ring() {
-    static_assert(KEEP > 0 && KEEP < 64, "vmcnt range");
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    asm volatile("; ssd ring wait" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(KEEP));
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
-
 // An L2 prefetch: one direct-to-LDS load of a 1 KB block (64 lanes x 16
 // bytes) into a scratch LDS block that nothing reads, issued only to bring
 // the block's lines into L2 ahead of the load that uses them.  The marker
