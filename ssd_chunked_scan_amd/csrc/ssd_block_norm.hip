@@ -20,6 +20,12 @@
 // With checkpoints (CKPT) x, z and s are also written as e4m3 with a scale
 // per 128 columns, and backward reads those instead: 13 bytes a column
 // instead of 16 in bf16, and 3 kept instead of 6.
+//
+// Measured, 16384 x 2560 bf16 with the gate (a copy reaches 4.8 TB/s): forward 91
+// us, 4.6 TB/s, and 122 with checkpoints, 4.5; backward 142, 4.7, and 125 from
+// checkpoints, 4.4.  4096 x 12288: 106, 153, 189 and 172.  Odd widths go column by
+// column: 30000 x 1003 72, 131, 112 and 113 (3.0 to 4.3), and past 8192 columns
+// with spills: 4096 x 12289 196, 333, 573 and 518.
 #include <algorithm>
 
 #include "ssd_block.hpp"
@@ -330,6 +336,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
     const float inv_n = 1.f / (float)a.columns;
     constexpr bool HOLD = block_bwd_holds(K, V);   // weights and sums in registers
     float w1[HOLD ? K : 1][V], w2[HOLD ? K : 1][V];
+    // Sixteen single columns leave no registers for the next row before this one is done.
+    constexpr bool LATE = V == 1 && K > 8;
     typedef ColumnSums<V, K, HOLD> CS;
     __shared__ __attribute__((aligned(16))) float column_sums[2][CS::kFloats];
     CS dm, dp;
@@ -359,7 +367,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
                 const __amdgpu_buffer_rsrc_t qb = row_of(q, r, a.columns, a.columns);
                 const __amdgpu_buffer_rsrc_t cb = row_of(sc, r, nscale * 4, nscale * 4);
 #pragma unroll
-                for (int k = 0; k < K; ++k) to[k] = load_kept<V>(qb, cb, pack_at<V>(k, tid, nthr));
+                for (int k = 0; k < K; ++k) {
+                    to[k] = load_kept<V>(qb, cb, pack_at<V>(k, tid, nthr));
+                    if (V == 1 && k % 2 == 1) to[k].scale = to[k - 1].scale;   // of one block
+                }
             };
             kept(xk, a.xq, a.xsc);
             kept(sk, a.sq, a.ssc);
@@ -439,7 +450,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
             buffer_store<IO, V>(rb, (uint32_t)(p * (V * E)), 0, dr);
             if (GATE) buffer_store<IO, V>(zb, (uint32_t)(p * (V * E)), 0, dz);
         }
-        load(min(row + step, a.rows - 1));
+        if constexpr (!LATE) load(min(row + step, a.rows - 1));
         row_sums<WAVE, 1>(sum, lds[1]);
         const float mean1 = sum[0] * inv_n;
         const __amdgpu_buffer_rsrc_t xb = row_of(a.dx, row, dense, bytes);
@@ -450,6 +461,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
             for (int v = 0; v < V; ++v) dx[v] = rstd1 * fmaf(-n1[k][v], mean1, h[k][v]);
             buffer_store<IO, V>(xb, (uint32_t)(pack_at<V>(k, tid, nthr) * (V * E)), 0, dx);
         }
+        if constexpr (LATE) load(min(row + step, a.rows - 1));
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * 2 * a.columns;
@@ -511,11 +523,11 @@ __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
 
 template <typename IO, int V, bool WAVE, int K>
 static void block_fwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
-    // as many workgroups as are resident: 28 waves a compute unit with
-    // checkpoints, whose registers leave room for no more (16384 x 2560: 126 us,
-    // 136 with 32), 32 without
+    // 28 waves a compute unit, which are resident whatever the variant's registers
+    // (16384 x 2560 with checkpoints 122 us, 128 with 32, 123 with 24; 8192 x 5120
+    // 87 without them, 89 with 32)
     const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
-    const int64_t fit = (int64_t)a.cus * std::max(1, (a.xq ? 28 : 32) / (nthr / 64));
+    const int64_t fit = (int64_t)a.cus * std::max(1, 28 / (nthr / 64));
     const dim3 grid((unsigned)std::min(rows, fit));
 #define SSD_BLOCK_FWD(G, C)                                                                                  \
     if (!a.z == !G && !a.xq == !C)                                                                           \
