@@ -15,13 +15,15 @@ struct BlockArgs {
     int64_t dys, drs;
     void *dx, *dz, *dresidual;          // backward
     float *dpost, *dpre, *dscale;       // backward, nullable
-    float *part;                        // backward: [parts][2][columns], null without a column sum to give
+    float *part;                        // backward: [parts][2][pitch], null without a column sum to give
     uint8_t *xq, *zq, *sq;              // checkpoints: e4m3 [rows][columns], null without
     float *xsc, *zsc, *ssc;             // [rows][ceil(columns / 128)]
     float eps, alpha;
     int64_t rows;
     int columns, cus;
+    int pitch;                          // columns up to whole packs of 8
     int parts;                          // backward: workgroups
+    bool code_words;                    // a checkpoint's rows of codes are whole 4-byte words
 };
 
 }  // namespace ssd

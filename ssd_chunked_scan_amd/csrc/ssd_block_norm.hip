@@ -21,11 +21,12 @@
 // per 128 columns, and backward reads those instead: 13 bytes a column
 // instead of 16 in bf16, and 3 kept instead of 6.
 //
-// Measured, 16384 x 2560 bf16 with the gate (a copy reaches 4.8 TB/s): forward 91
-// us, 4.6 TB/s, and 122 with checkpoints, 4.5; backward 142, 4.7, and 125 from
-// checkpoints, 4.4.  4096 x 12288: 106, 153, 189 and 172.  Odd widths go column by
-// column: 30000 x 1003 72, 131, 112 and 113 (3.0 to 4.3), and past 8192 columns
-// with spills: 4096 x 12289 196, 333, 573 and 518.
+// Measured, 16384 x 2560 bf16 with the gate (a copy reaches 4.8 TB/s): forward 89
+// us, 4.7 TB/s, and 122 with checkpoints, 4.5; backward 142, 4.7, and 123 from
+// checkpoints, 4.4.  4096 x 12288: 106, 152, 187 and 168.  fp32 5000 x 5001: 107,
+// 131, 163 and 154.  Odd bf16 rows go column by column: 30000 x 1003 70, 132, 110
+// and 111 (3.0 to 4.4), and past 8192 columns with spills: 4096 x 12289 196, 333,
+// 570 and 525.
 #include <algorithm>
 
 #include "ssd_block.hpp"
@@ -57,15 +58,20 @@ __device__ inline void row_sums(float (&v)[N], float *lds) {
 
 // A row of a tensor through a buffer descriptor that ends with its last column:
 // what lies past it is read as 0 and not written, so that no lane needs a
-// branch, and a tensor that is not given (bytes 0) reads as 0 throughout.
+// branch, and a tensor that is not given (bytes 0) reads as 0 throughout.  That
+// goes by 4-byte words, and wide accesses need no more alignment than a word: rows
+// whose bytes are not a multiple of 16 take them too.
 __device__ inline __amdgpu_buffer_rsrc_t row_of(const void *base, int64_t row, int64_t stride, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(base) + row * stride, 0, bytes, 0x00027000);
 }
 
-// A row's values as e4m3 with a scale per 128 columns.
-template <int V, int K>
-__device__ inline void store_checkpoint(__amdgpu_buffer_rsrc_t q, __amdgpu_buffer_rsrc_t sc, const float (&val)[K][V], int tid,
-                                        int nthr) {
+// A row's values as e4m3 with a scale per 128 columns.  WORDS: rows of codes begin
+// at 4-byte words; elsewhere stores go by the address, which may be any.
+template <int V, int K, bool WORDS>
+__device__ inline void store_checkpoint(const BlockArgs &a, uint8_t *codes, float *scales, int64_t row, const float (&val)[K][V],
+                                        int tid, int nthr) {
+    const int nscale = (a.columns + 127) / 128;
+    const __amdgpu_buffer_rsrc_t q = row_of(codes, row, a.columns, a.columns), sc = row_of(scales, row, nscale * 4, nscale * 4);
     constexpr int PER = V == 1 ? 2 : 1, LANES = V == 1 ? 64 : 128 / V;
 #pragma unroll
     for (int k = 0; k < K; k += PER) {
@@ -86,10 +92,16 @@ __device__ inline void store_checkpoint(__amdgpu_buffer_rsrc_t q, __amdgpu_buffe
             store_e4m3<V>(code, val[k + j], inv);
             if constexpr (V == 1) {
                 __builtin_amdgcn_raw_buffer_store_b8(code[0], q, at, 0, 0);
-            } else if constexpr (V == 4) {
+            } else if constexpr (WORDS && V == 4) {
                 __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(Pack<uint32_t, 1>, code).v[0], q, at, 0, 0);
-            } else {
+            } else if constexpr (WORDS) {
                 __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(Words<8>::type, code), q, at, 0, 0);
+            } else if ((int)at + V <= a.columns) {
+                typedef uint32_t __attribute__((ext_vector_type(V / 4), aligned(1), may_alias)) piece;
+                *(piece *)(codes + row * a.columns + at) = __builtin_bit_cast(piece, code);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) __builtin_amdgcn_raw_buffer_store_b8(code[v], q, at + v, 0, 0);
             }
         }
     }
@@ -166,7 +178,8 @@ __device__ inline void block_weights(const BlockArgs &a, int p, float (&w1)[V], 
     for (int v = 0; v < V; ++v) w1[v] *= scale[v];
 }
 
-template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
+// CKPT: 1 with checkpoints, 2 with ones whose rows of codes are not whole words.
+template <typename IO, int V, bool WAVE, int K, bool GATE, int CKPT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs a) {
     typedef Raw<IO, V> RW;
     typedef typename RW::type R;
@@ -174,7 +187,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
     constexpr int E = (int)sizeof(IO);
     __shared__ float lds[2][16];
     const int tid = WAVE ? threadIdx.x % 64 : threadIdx.x, nthr = WAVE ? 64 : blockDim.x;
-    const int nscale = (a.columns + 127) / 128, bytes = a.columns * E, dense = bytes;
+    const int bytes = a.columns * E, dense = bytes;
     const float inv_n = 1.f / (float)a.columns;
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
@@ -211,19 +224,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
                 val[k][v] = RW::at(xr[k], v);
                 sum[0] = fmaf(val[k][v], val[k][v], sum[0]);
             }
-        if constexpr (CKPT)
-            store_checkpoint<V, K>(row_of(a.xq, row, a.columns, a.columns), row_of(a.xsc, row, nscale * 4, nscale * 4), val, tid,
-                                   nthr);
+        if constexpr (CKPT != 0)
+            store_checkpoint<V, K, CKPT == 1>(a, a.xq, a.xsc, row, val, tid, nthr);
         row_sums<WAVE, 1>(sum, lds[0]);
         const float rstd1 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
-        if constexpr (CKPT && GATE) {
+        if constexpr (CKPT != 0 && GATE) {
             float z[K][V];
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) z[k][v] = RW::at(zr[k], v);
-            store_checkpoint<V, K>(row_of(a.zq, row, a.columns, a.columns), row_of(a.zsc, row, nscale * 4, nscale * 4), z, tid,
-                                   nthr);
+            store_checkpoint<V, K, CKPT == 1>(a, a.zq, a.zsc, row, z, tid, nthr);
         }
         sum[0] = 0.f;
         const __amdgpu_buffer_rsrc_t ro = row_of(a.residual_out, row, dense, bytes);
@@ -247,9 +258,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_fwd_kernel(BlockArgs 
             }
             buffer_store<IO, V>(ro, (uint32_t)(p * (V * E)), 0, st);
         }
-        if constexpr (CKPT)
-            store_checkpoint<V, K>(row_of(a.sq, row, a.columns, a.columns), row_of(a.ssc, row, nscale * 4, nscale * 4), val, tid,
-                                   nthr);
+        if constexpr (CKPT != 0)
+            store_checkpoint<V, K, CKPT == 1>(a, a.sq, a.ssc, row, val, tid, nthr);
         if constexpr (!HOLD) load(min(row + step, a.rows - 1), xr, rr, zr);
         row_sums<WAVE, 1>(sum, lds[1]);
         const float rstd2 = 1.f / __builtin_sqrtf(fmaf(sum[0], inv_n, a.eps));
@@ -321,7 +331,7 @@ struct ColumnSums {
 constexpr bool block_bwd_holds(int K, int V) { return K * V <= (V == 1 ? 4 : 8); }
 
 // Backward: a.parts workgroups take the rows in turn and keep their columns'
-// two sums; each leaves a row of parts [2][columns]: m, dpre.
+// two sums; each leaves a row of parts [2][pitch]: m, dpre.
 template <typename IO, int V, bool WAVE, int K, bool GATE, bool CKPT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) void block_bwd_kernel(BlockArgs a) {
     typedef Raw<IO, V> RW;
@@ -464,7 +474,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
         if constexpr (LATE) load(min(row + step, a.rows - 1));
     }
     if (!a.part) return;
-    float *out = a.part + (int64_t)blockIdx.x * 2 * a.columns;
+    float *out = a.part + (int64_t)blockIdx.x * 2 * a.pitch;
     if constexpr (WAVE) {
         auto join = [&](const float (&d)[K][V], float *to) {
 #pragma unroll
@@ -477,7 +487,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
             __syncthreads();
         };
         join(dm.r, out);
-        join(dp.r, out + a.columns);
+        join(dp.r, out + a.pitch);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -489,7 +499,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, block_bwd_holds(K, V) ? 4 : 1) v
             for (int v = 0; v < V; ++v)
                 if (p * V < a.columns) {
                     out[p * V + v] = m[v];
-                    out[a.columns + p * V + v] = q[v];
+                    out[a.pitch + p * V + v] = q[v];
                 }
         }
     }
@@ -504,10 +514,10 @@ __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
     const int lane = threadIdx.x % kFinish, run = threadIdx.x / kFinish, n = a.columns;
     const int ncol = (n + kFinish - 1) / kFinish, plane = blockIdx.x / ncol, c = blockIdx.x % ncol * kFinish + lane;
     const int per = (a.parts + kFinish - 1) / kFinish, k0 = min(run * per, a.parts), k1 = min(k0 + per, a.parts);
-    const float *p = a.part + (int64_t)plane * n + min(c, n - 1);
+    const float *p = a.part + (int64_t)plane * a.pitch + min(c, n - 1);
     float acc = 0.f;
 #pragma unroll 8
-    for (int k = k0; k < k1; ++k) acc += p[(int64_t)k * 2 * n];
+    for (int k = k0; k < k1; ++k) acc += p[(int64_t)k * 2 * a.pitch];
     s[run][lane] = acc;
     __syncthreads();
     if (run == 0 && c < n) {
@@ -529,13 +539,18 @@ static void block_fwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
     const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
     const int64_t fit = (int64_t)a.cus * std::max(1, 28 / (nthr / 64));
     const dim3 grid((unsigned)std::min(rows, fit));
+    const int ckpt = !a.xq ? 0 : V == 1 || a.code_words ? 1 : 2;
 #define SSD_BLOCK_FWD(G, C)                                                                                  \
-    if (!a.z == !G && !a.xq == !C)                                                                           \
+    if (!a.z == !G && ckpt == C)                                                                             \
         hipLaunchKernelGGL((block_fwd_kernel<IO, V, WAVE, K, G, C>), grid, dim3(nthr), 0, stream, a);
-    SSD_BLOCK_FWD(false, false)
-    SSD_BLOCK_FWD(false, true)
-    SSD_BLOCK_FWD(true, false)
-    SSD_BLOCK_FWD(true, true)
+    SSD_BLOCK_FWD(false, 0)
+    SSD_BLOCK_FWD(false, 1)
+    SSD_BLOCK_FWD(true, 0)
+    SSD_BLOCK_FWD(true, 1)
+    if constexpr (V > 1) {
+        SSD_BLOCK_FWD(false, 2)
+        SSD_BLOCK_FWD(true, 2)
+    }
 #undef SSD_BLOCK_FWD
 }
 
@@ -556,7 +571,7 @@ static void block_bwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
 // workgroup of KB, KM or KX packs a thread, the first with which 1024 threads can
 // hold the row.
 #define SSD_BLOCK_SHAPE(launch)                                        \
-    const int npack = a.columns / V;                                   \
+    const int npack = (a.columns + V - 1) / V;                         \
     if (npack <= 64 * KW)                                              \
         launch<IO, V, true, KW>(a, stream, 256);                       \
     else if (npack <= 1024 * KB)                                       \

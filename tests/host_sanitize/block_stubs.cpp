@@ -47,7 +47,7 @@ int compute_units(hipStream_t) { return 256; }
 static void block_common(bool bf16_io, bool wide, const BlockArgs &a) {
     ++g_block_launches;
     const size_t e = bf16_io ? 2 : 4, D = a.columns;
-    if (a.cus <= 0 || (wide && D % (16 / e) != 0)) __builtin_trap();
+    if (a.cus <= 0 || (wide && D * e % 4 != 0)) __builtin_trap();
     rd_rows(a.x, a.rows, a.xs, D * e);
     rd_rows(a.z, a.rows, a.zs, D * e);
     rd_rows(a.residual, a.rows, a.rs, D * e);
@@ -81,7 +81,7 @@ void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t) 
     rd(a.ssc, 4 * a.rows * nb);
     rd_rows(a.dy, a.rows, a.dys, D * e);
     rd_rows(a.dresidual_out, a.rows, a.drs, D * e);
-    wr(a.part, 4 * (size_t)a.parts * 2 * D);
+    wr(a.part, 4 * (size_t)a.parts * 2 * ((D + 7) / 8 * 8));
     wr(a.dx, a.rows * D * e);
     wr(a.dz, a.rows * D * e);
     wr(a.dresidual, a.rows * D * e);

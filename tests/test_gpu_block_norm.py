@@ -67,6 +67,10 @@ CASES = [
     (3, 8200, "bf16", True, 7, 1.0, None), (3, 8195, "f32", True, 7, 1.0, None), (2, 16384, "bf16", True, 7, 1.0, None),
     (2, 16384, "f32", True, 7, 1.0, None), (2, 16383, "bf16", True, 7, 1.0, None), (2, 16381, "f32", False, 7, 1.0, 3),
     (9000, 96, "bf16", True, 7, 1.0, None), (2900, 640, "bf16", True, 7, 1.0, None), (2200, 1003, "f32", True, 7, 1.0, None),
+    # rows of whole 4-byte words that are not whole 16-byte pieces
+    (7, 2, "bf16", True, 7, 1.0, None), (40, 510, "bf16", True, 7, 1.0, 2), (33, 1002, "bf16", True, 7, 1.0, None),
+    (9, 4098, "bf16", True, 7, 1.0, 2), (5, 6003, "f32", True, 7, 1.0, 3), (5, 12290, "bf16", True, 7, 1.0, None),
+    (5, 12292, "bf16", False, 5, 0.5, 4), (5, 12289, "f32", True, 7, 1.0, 1), (900, 4101, "f32", True, 7, 1.0, None),
 ]
 
 
