@@ -594,11 +594,17 @@ static void mx4_few_launch(const Mx4ProductArgs &a, hipStream_t stream) {
         hipLaunchKernelGGL((mx4_few_kernel<IN, OUT, MT, NT, W>), dim3((a.n + 16 * NT - 1) / (16 * NT)), dim3(64 * W), 0,
                            stream, a);
     };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
     const std::integral_constant<int, 8> eight;
-    if (fits(4)) launch(std::integral_constant<int, 4>{}, eight);
-    else if (fits(2)) launch(std::integral_constant<int, 2>{}, eight);
-    else if (!std::is_same_v<IN, uint8_t> && a.kblocks > 8) launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
-    else launch(std::integral_constant<int, 1>{}, eight);
+    if constexpr (MT == 1) {   // (more tokens come this way with few outputs only)
+        if (fits(4)) return launch(std::integral_constant<int, 4>{}, eight);
+    }
+    if (fits(2)) return launch(two, eight);
+    if constexpr (!std::is_same_v<IN, uint8_t>) {
+        if (a.kblocks > 8) return launch(one, std::integral_constant<int, 16>{});
+    }
+    launch(one, eight);
 }
 
 template <typename OUT>
