@@ -560,9 +560,12 @@ static void block_bwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
 #define SSD_BLOCK_BWD(G, C)                                                                                  \
     if (!a.dz == !G && !a.xq == !C)                                                                          \
         hipLaunchKernelGGL((block_bwd_kernel<IO, V, WAVE, K, G, C>), grid, dim3(nthr), 0, stream, a);
-    SSD_BLOCK_BWD(false, false)
+    // (whole fp32 rows of more than 4096 columns always go in packs)
+    if constexpr (sizeof(IO) == 2 || V > 1 || K <= 4) {
+        SSD_BLOCK_BWD(false, false)
+        SSD_BLOCK_BWD(true, false)
+    }
     SSD_BLOCK_BWD(false, true)
-    SSD_BLOCK_BWD(true, false)
     SSD_BLOCK_BWD(true, true)
 #undef SSD_BLOCK_BWD
 }
@@ -590,8 +593,8 @@ static void block_bwd_shape(const BlockArgs &a, hipStream_t stream) { SSD_BLOCK_
 void launch_block_fwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {
     if (bf16_io)
         wide ? block_fwd_shape<bf16, 8, 1, 1, 1, 2>(a, stream) : block_fwd_shape<bf16, 1, 8, 8, 8, 16>(a, stream);
-    else
-        wide ? block_fwd_shape<float, 4, 2, 2, 2, 4>(a, stream) : block_fwd_shape<float, 1, 8, 8, 8, 16>(a, stream);
+    else   // (fp32 rows are whole words)
+        block_fwd_shape<float, 4, 2, 2, 2, 4>(a, stream);
 }
 
 void launch_block_bwd(bool bf16_io, bool wide, const BlockArgs &a, hipStream_t stream) {

@@ -19,6 +19,10 @@ CASES = [
     (900, 12288, "bf16", True, 7, 1.0, None), (900, 12288, "f32", True, 7, 1.0, None), (900, 12289, "bf16", True, 7, 1.0, None),
     (900, 12289, "f32", True, 7, 1.0, None), (900, 5001, "bf16", True, 7, 1.0, None), (900, 12290, "bf16", False, 7, 0.5, None),
     (900, 9001, "bf16", False, 7, 0.5, 1), (900, 9001, "f32", False, 7, 0.5, 1),
+    # without a gate, in the widths that the other cases have with one only
+    (40, 129, "bf16", False, 7, 1.0, None), (40, 510, "bf16", False, 7, 1.0, None), (1100, 1002, "bf16", False, 7, 1.0, None),
+    (1100, 1003, "bf16", False, 7, 0.5, 1), (700, 5001, "bf16", False, 7, 1.0, None), (300, 6003, "f32", False, 7, 1.0, None),
+    (600, 12288, "f32", False, 7, 1.0, None),
 ]
 
 
@@ -49,9 +53,10 @@ def untouched(room, t, off):
 # and a workgroup a row, one to sixteen columns a thread
 ADDRESSES = [(96, "bf16"), (96, "f32"), (2560, "bf16"), (2560, "f32"), (2562, "bf16"), (1003, "bf16"), (1003, "f32"), (4104, "bf16"),
              (4100, "f32"), (8200, "bf16"), (8200, "f32"), (12288, "bf16")]
+OFFSETS = [(1, 0), (0, 1), (2, 3), (3, 2)]
 
 
-@pytest.mark.parametrize("off,codes", [(1, 0), (0, 1), (2, 3), (3, 2)])
+@pytest.mark.parametrize("off,codes", OFFSETS)
 @pytest.mark.parametrize("columns,dtype", ADDRESSES)
 def test_outputs_and_checkpoints_at_any_address(columns, dtype, off, codes):
     """y, the stream and the gradients `off` elements behind a 16-byte boundary, a

@@ -71,3 +71,54 @@ def test_products():
     assert sorted(reached) == ["mx4_few_kernel", "mx4_ring_kernel", "mx4_tile_kernel"]
     for kernel, variants in reached.items():
         assert built(kernel) == variants, (kernel, built(kernel) ^ variants)
+
+
+# -------------------------------------------------------------- block norm
+
+
+def block_variant(columns, io, gate, kept, wide, backward, code_words):
+    single = (8, 8, 8, 16) if not backward else (4, 4, 8, 16)   # packs: a wave's lane, then a workgroup's thread
+    V, packs = (1, single) if not wide else (8, (1, 1, 1, 2)) if io == "bf16" else (4, (2, 2, 2, 4))
+    npack = ceil(columns, V)
+    wave = npack <= 64 * packs[0]
+    K = packs[0] if wave else next(k for k in packs[1:] if npack <= 1024 * k or k == packs[-1])
+    how = int(kept) if backward else 0 if not kept else 1 if V == 1 or code_words else 2
+    return io, V, int(wave), K, int(gate), how
+
+
+def block(rows, columns, io, gate, pad=None, off=0, codes=0):
+    """The kernels of a forward and a backward call without and with checkpoints:
+    inputs `pad` elements inside wider rows, outputs `off` elements and codes
+    `codes` bytes off a 16-byte boundary."""
+    e = 2 if io == "bf16" else 4
+    code_words = columns % 4 == 0 and codes % 4 == 0
+
+    def fit(nbytes, *addresses):
+        rows_in = (pad or 0) * e, (columns + 2 * (pad or 0)) * e
+        return all(a % nbytes == 0 for a in (columns * e, *rows_in, *addresses))
+
+    for kept in (False, True):
+        wide = io == "f32" or fit(4, off * e)
+        yield "block_fwd_kernel", block_variant(columns, io, gate, kept, wide, False, code_words)
+        wide = (not kept or code_words) and fit(16 if columns <= 4096 else 4, off * e)
+        yield "block_bwd_kernel", block_variant(columns, io, gate, kept, wide, True, code_words)
+
+
+def block_cases():
+    import test_gpu_block_norm as norm
+    import test_gpu_block_rows as more
+    for rows, columns, io, gate, _, _, pad in norm.CASES + more.CASES:
+        yield rows, columns, io, gate, pad
+    for columns, io in more.ADDRESSES:
+        for off, codes in more.OFFSETS:
+            yield 21, columns, io, True, None, off, codes
+
+
+def test_block_norm():
+    reached = {}
+    for case in block_cases():
+        for kernel, variant in block(*case):
+            reached.setdefault(kernel, set()).add(variant)
+    for kernel, variants in reached.items():
+        made = built(kernel)
+        assert made == variants, (kernel, "not reached", sorted(made - variants), "not built", sorted(variants - made))
