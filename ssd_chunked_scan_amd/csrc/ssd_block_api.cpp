@@ -35,16 +35,19 @@ ssd_status_t check_block(const ssd_block_shape_t *s, ssd_dtype_t io) {
 }
 
 // Workgroups of the backward kernel, each one part of the column sums: twelve
-// waves for each compute unit, and at most one workgroup a row.  More rows at
-// once hide more latency but leave more parts to sum (16384 x 2560: 142 us with
-// 2 workgroups of 5 waves for each compute unit, 158 with 3, 168 with 1; 8192 x
-// 5120: 145 with 1 of 10, 158 with 2; 30000 x 1003: 107 with 3 of 4, 124 with
-// 2, 116 with 4).  `wide`: 16-byte accesses, eight columns a thread up to 8192
-// columns, else four up to 4096 and eight up to 8192; sixteen past those.
+// waves for each compute unit, and at most one workgroup for each row, or for each
+// four where a wave takes a row.  More rows at once hide more latency but leave
+// more parts to sum (16384 x 2560: 142 us with 2 workgroups of 5 waves for each
+// compute unit, 158 with 3, 168 with 1; 8192 x 5120: 145 with 1 of 10, 158 with 2;
+// 30000 x 1003: 107 with 3 of 4, 124 with 2, 116 with 4).  `wide`: 16-byte
+// accesses, eight columns a thread up to 8192 columns, else four up to 4096 and
+// eight up to 8192; sixteen past those.
 int block_parts(const ssd_block_shape_t *s, bool wide, hipStream_t stream) {
     const int64_t per = s->columns > 8192 ? 16 : wide || s->columns > 4096 ? 8 : 4;
-    const int64_t waves = s->columns <= (wide ? 512 : 256) ? 4 : (s->columns + 64 * per - 1) / (64 * per);
-    return (int)std::min<int64_t>(std::max<int64_t>(1, 12 / waves) * ssd::compute_units(stream), s->rows);
+    const bool wave_rows = s->columns <= (wide ? 512 : 256);
+    const int64_t waves = wave_rows ? 4 : (s->columns + 64 * per - 1) / (64 * per);
+    return (int)std::min<int64_t>(std::max<int64_t>(1, 12 / waves) * ssd::compute_units(stream),
+                                  wave_rows ? (s->rows + 3) / 4 : s->rows);
 }
 
 // For either access, which the buffers' alignment decides.
