@@ -586,8 +586,8 @@ typedef struct {
     int64_t reserved[4];  /* must be zero                                */
 } ssd_mx4_shape_t;
 
-/* x: io dtype.  rows / 16 times columns / 512, each rounded up, is
- * less than 2^24. */
+/* x: io dtype.  Here and in the calls below rows / 16 times columns / 512, each
+ * rounded up, is less than 2^24. */
 ssd_status_t ssd_mx4_quant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const void *x,
                            void *q, void *scales, void *stream);
 
@@ -600,7 +600,7 @@ ssd_status_t ssd_mx4_dequant(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
  * wq and wscales [outputs], both of `columns` columns; products of codes exact,
  * sums in fp32, y [rows][outputs] in the io dtype, dense; bias [outputs]
  * fp32, nullable.  rows / 64 times outputs / 64, each rounded up, is less than
- * 2^24.  No workspace. */
+ * 2^24 too.  No workspace. */
 ssd_status_t ssd_mx4_matmul(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
                             const void *q, const void *scales,
                             const void *wq, const void *wscales, const float *bias,
