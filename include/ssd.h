@@ -591,8 +591,10 @@ typedef struct {
 ssd_status_t ssd_mx4_quant(const ssd_mx4_shape_t *shape, ssd_dtype_t io, const void *x,
                            void *q, void *scales, void *stream);
 
-/* The values that q and scales stand for, in the io dtype (which holds them
- * exactly), dense. */
+/* The values that q and scales stand for, in the io dtype, dense.  Either type
+ * holds them exactly for scale bytes up to 252, which is all that ssd_mx4_quant
+ * writes but for 255; with 253 and 254 those past the largest number become
+ * infinities. */
 ssd_status_t ssd_mx4_dequant(const ssd_mx4_shape_t *shape, ssd_dtype_t io,
                              const void *q, const void *scales, void *y, void *stream);
 

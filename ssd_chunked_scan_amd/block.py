@@ -233,7 +233,9 @@ def ssd_mx4_quant(x, q=None, scales=None, stream=None) -> Tuple["torch.Tensor", 
 
 def ssd_mx4_dequant(q, scales, columns: int, dtype=None, y=None, stream=None) -> "torch.Tensor":
     """The values of ssd_mx4_quant's codes: [..., columns] in ``dtype``, bfloat16
-    (the default) or float32, either of which holds them exactly."""
+    (the default) or float32, either of which holds them exactly.  (Codes from
+    elsewhere may have scale bytes 253 and 254: values past the largest number
+    become infinities.)"""
     lib = layer._library()
     name = "ssd_mx4_dequant"
     dev = _mx4_device(name, q)
