@@ -67,6 +67,10 @@ def _block_common(name, x, z, post_weight, pre_weight, scale, alpha, eps):
 _KEPT = ("x", "z", "residual")
 
 
+def _has_gate(checkpoint):
+    return checkpoint.get("z_q") is not None or checkpoint.get("z_scales") is not None
+
+
 def _checkpoint(given, like, gate):
     """The dict of a checkpoint's tensors, new or checked, and its structure."""
     torch = layer.torch
@@ -74,9 +78,11 @@ def _checkpoint(given, like, gate):
     scales = (*shape[:-1], -(-shape[-1] // 128))
     fields, out = {}, {}
     for name in _KEPT:
-        if name == "z" and not gate:
-            continue
         q, s = name + "_q", name + "_scales"
+        if name == "z" and not gate:
+            if given is not None and _has_gate(given):
+                raise ValueError("checkpoint: z_q and z_scales are given without a gate")
+            continue
         if given is None:
             out[q] = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
             out[s] = torch.empty(scales, dtype=torch.float32, device=dev)
@@ -142,7 +148,7 @@ def ssd_block_norm_bwd(x, residual_out, post_weight, pre_weight, dy, z=None, sca
     if checkpoint is not None:
         if x is not None or residual_out is not None or z is not None:
             raise ValueError(f"{name}: a checkpoint stands for x, residual_out and z")
-        gate = checkpoint.get("z_q") is not None
+        gate = _has_gate(checkpoint)
         _, struct = _checkpoint(checkpoint, dy, gate)
         struct = ctypes.byref(struct)
     else:
