@@ -533,9 +533,12 @@ __global__ __launch_bounds__(1024) void block_finish_kernel(BlockArgs a) {
 
 template <typename IO, int V, bool WAVE, int K>
 static void block_fwd_launch(const BlockArgs &a, hipStream_t stream, int nthr) {
-    // 28 waves a compute unit, which are resident whatever the variant's registers
-    // (16384 x 2560 with checkpoints 122 us, 128 with 32, 123 with 24; 8192 x 5120
-    // 87 without them, 89 with 32)
+    // 28 waves a compute unit, for which bf16 rows in packs of 8 of up to 8192
+    // columns have the registers (16384 x 2560 with checkpoints 122 us, 128 with
+    // 32, 123 with 24; 8192 x 5120 87 without them, 89 with 32).  Other variants
+    // have them for less, 16 to 24 waves: single columns, codes that are not whole
+    // words, and most of fp32 and of more than 8192 columns with a gate or
+    // checkpoints.  Their last workgroups start when the first ones end.
     const int64_t rows = WAVE ? (a.rows + 3) / 4 : a.rows;
     const int64_t fit = (int64_t)a.cus * std::max(1, 28 / (nthr / 64));
     const dim3 grid((unsigned)std::min(rows, fit));
