@@ -342,11 +342,13 @@ __global__ __launch_bounds__(256) void mx4_ring_kernel(Mx4ProductArgs a, int til
 //    loads every stage, the other half stores every result, its partner's
 //    chunk by chunk through LDS (293 us before, 262 after).
 //  - `group` rows of tiles column by column, four of them: neighbouring pieces
-//    of y's rows meet in one XCD's L2 (262 us with eight, 218 with four).  Each such group
-//    begins at another column: y's rows below each other lie a multiple of
-//    large powers of two apart, and side by side the XCDs would write to few of
-//    the memory's channels (new results every time, 259 us before, 247 after;
-//    8192 rows 149 and 131).
+//    of y's rows meet in one XCD's L2 (230 us with four, 237 with eight, 233 with
+//    two, 250 with one; 8192 x 8192 x 8192 221, 223, 225, 235; 16384 x 2560 x 5120
+//    98 to 99 with any).  Each such group begins at another column: y's rows below
+//    each other lie a multiple of large powers of two apart, and side by side the
+//    XCDs would write to few of the memory's channels.  That is seen behind the
+//    quantisation of x (252 us before, 247 after; 8192 rows 131 and 125; 8192 x 8192
+//    x 8192 263 and 255), not in the product alone.
 // The stage of an odd last 128 columns is the last 256 once more with the scales
 // of the first half, which has been taken, at 2^-127: a product below 2^-240 in
 // place of each, which fp32 sums round away.
