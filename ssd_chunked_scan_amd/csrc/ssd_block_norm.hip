@@ -22,11 +22,12 @@
 // instead of 16 in bf16, and 3 kept instead of 6.
 //
 // Measured, 16384 x 2560 bf16 with the gate (a copy reaches 4.8 TB/s): forward 89
-// us, 4.7 TB/s, and 122 with checkpoints, 4.5; backward 142, 4.7, and 123 from
-// checkpoints, 4.4.  4096 x 12288: 106, 152, 187 and 168.  fp32 5000 x 5001: 107,
-// 131, 163 and 154.  Odd bf16 rows go column by column: 30000 x 1003 70, 132, 110
-// and 111 (3.0 to 4.4), and past 8192 columns with spills: 4096 x 12289 196, 333,
-// 570 and 525.
+// us, 4.7 TB/s, and 121 with checkpoints, 4.5; backward 143, 4.7, and 126 from
+// checkpoints, 4.3.  4096 x 12288: 106, 151, 186 and 170.  fp32 5000 x 5001: 107,
+// 131, 162 and 154.  Odd bf16 rows, and codes of odd rows backward, go column by
+// column: 30000 x 1003 70, 132, 110 and 111 (3.0 to 4.4 TB/s), 5000 x 5001 62, 128,
+// 128 and 145 (2.2 to 4.0), and past 8192 columns with up to 83 registers spilled:
+// 4096 x 12289 196, 334, 570 and 525, fp32 from checkpoints 457.
 #include <algorithm>
 
 #include "ssd_block.hpp"

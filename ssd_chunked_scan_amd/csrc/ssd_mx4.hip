@@ -1,6 +1,6 @@
 // Microscaled 4-bit floating point: to 4 bits and back (ssd.h, ssd_mx4_quant,
-// ssd_mx4_dequant).  Memory-bound: 16384 x 5120 bf16 39 us, 5.5 TB/s, and 41 back;
-// 10576 x 2560, which the caches hold in part, 11.8 and 11.8.  Sixteen lanes take
+// ssd_mx4_dequant).  Memory-bound: 16384 x 5120 bf16 40 us, 5.3 TB/s, and 43 back;
+// 10576 x 2560, which the caches hold in part, 12 and 12.  Sixteen lanes take
 // 128 columns of a row, eight each: a block of 32 is a quad of lanes, its maximum
 // two lane exchanges, and the four scale bytes of the 128 columns are joined into
 // one word.
